@@ -352,6 +352,145 @@ sas_status sas_decode_paged_noalloc(const void *q, const void *k_cache, const vo
                                     const float *log_gate, float sm_scale, void *o, float *lse,
                                     void *stream);
 
+/* Bytes of device workspace sas_decode_paged_q8 needs (0 on a bad argument). */
+size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
+
+/*
+ * sas_decode_paged_q8 - sas_decode_paged over 8-bit pages. The SAS pages have no
+ * counterpart: it halves the bytes of the cache that a decode step reads.
+ *
+ * k_cache, v_cache  device e4m3 codes (one byte each: 1 sign, 4 exponent and 3
+ *            mantissa bits, no infinities) [num_pages, Hkv, 64, D], 16-byte aligned.
+ * k_scale, v_scale  device fp32 [num_pages, Hkv]: key = k_scale * code, value =
+ *            v_scale * code, for the rows of that page and KV head. Between 2^-100
+ *            and 2^120 for every page that is read; any other scale is flagged and
+ *            its block skipped, like a bad page id.
+ * kv_len     as in sas_decode_paged; 0 is a padding entry: o 0, lse -inf, not flagged.
+ * Other arguments as in sas_decode_paged. Logits, softmax sums and accumulators are
+ * fp32; probabilities are rounded to fp16 in front of the value product. A sequence
+ * without a readable block gets o 0 and lse -inf.
+ * workspace  device, ws_bytes >= sas_decode_q8_workspace_size(...), 256-byte
+ *            aligned; contents on entry do not matter.
+ * SAS_ERR_UNSUPPORTED unless D = 128, page_size = 64 and the GQA group size is at
+ * most 8, and for num_pages * Hkv * 64 above 2^31 - 1.
+ */
+sas_status sas_decode_paged_q8(const void *q, const void *k_cache, const void *v_cache,
+                               const float *k_scale, const float *v_scale, int num_pages,
+                               const int32_t *page_table, int max_pages, const int32_t *kv_len,
+                               int N, int Hq, int Hkv, int D, int page_size, int K,
+                               const int32_t *idx, const int32_t *cnt, const float *log_gate,
+                               float sm_scale, void *o, float *lse,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * sas_qk_norm_rope - per-head RMS norm of queries and keys with the rotary position
+ * embedding in the same pass: what stands between the projections and sas_attn_fwd in
+ * the models the SAS pages train (Qwen3 attention layers). For each head row x of token
+ * row t at position p:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight,
+ *   y[i] = n[i] c[i] - n[i + D/2] s[i],  y[i + D/2] = n[i + D/2] c[i] + n[i] s[i]
+ * for i < D/2, with c, s from row p of the table; fp32 arithmetic, rounded once.
+ *
+ * dtype      SAS_BF16 or SAS_F32: q, k, the weights and the outputs.
+ * q, k       device [T, Hq, D], [T, Hkv, D]; each token's heads are contiguous, ld_q and
+ *            ld_k values lie between tokens (>= H * D; so q and k may be parts of one
+ *            fused projection's output). Bases and strides 16-byte aligned. T >= 0.
+ * q_weight, k_weight  device [D] of dtype, 16-byte aligned; both NULL: rotation only.
+ * rope_table device fp32 [max_pos, D]: row p holds D/2 cosines, then D/2 sines, of
+ *            position p's angles; 16-byte aligned.
+ * positions  device int32 [T], or NULL: token row t has position t % S. A position
+ *            outside 0 .. max_pos-1 is flagged and its output rows are zero.
+ * q_out, k_out  device [T, Hq, D], [T, Hkv, D], contiguous, 16-byte aligned (output);
+ *            they must not overlap the inputs.
+ * D in {64, 128}; T x heads up to 2^31 - 1. eps > 0.
+ */
+sas_status sas_qk_norm_rope(sas_dtype dtype, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                            const void *q_weight, const void *k_weight, const float *rope_table,
+                            int max_pos, const int32_t *positions, int S, int64_t T, int Hq, int Hkv,
+                            int D, float eps, void *q_out, void *k_out, void *stream);
+
+/* Bytes of device workspace sas_qk_norm_rope_bwd needs (0 on a bad argument). */
+size_t sas_qk_norm_rope_bwd_workspace_size(int64_t T, int Hq, int Hkv, int D);
+
+/*
+ * sas_qk_norm_rope_bwd - gradients of sas_qk_norm_rope with respect to q, k and the
+ * weights. q, k, weights, table and positions as in the forward (nothing else is saved).
+ *
+ * dq_out, dk_out  device [T, Hq, D], [T, Hkv, D] of dtype, contiguous: upstream gradients.
+ * dq, dk     device, of dtype, contiguous (output); rows of a flagged position are zero.
+ *            They must not overlap the inputs.
+ * dq_weight, dk_weight  device fp32 [D] (output): sums over all tokens and heads; given
+ *            if and only if the weights are. Sums are taken in a fixed order for a given
+ *            device and sizes, so results do not vary between runs.
+ * workspace  device, 256-byte aligned, ws_bytes >= sas_qk_norm_rope_bwd_workspace_size;
+ *            contents on entry do not matter.
+ */
+sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void *dk_out,
+                                const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *q_weight, const void *k_weight, const float *rope_table,
+                                int max_pos, const int32_t *positions, int S, int64_t T, int Hq, int Hkv,
+                                int D, float eps, void *dq, void *dk, float *dq_weight,
+                                float *dk_weight, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * sas_append_paged - new tokens into a paged KV cache, with the head norm and the rotary
+ * position embedding of sas_qk_norm_rope applied to q and k on the way (v is stored as it
+ * is). One call serves single tokens (decode) and prompts or pieces of them.
+ *
+ * q, k, v    device bf16 [T, Hq, D], [T, Hkv, D], [T, Hkv, D], token strides ld_q, ld_k,
+ *            ld_v as in sas_qk_norm_rope. q and q_out may both be NULL.
+ * q_weight, k_weight, rope_table, max_pos, eps   as in sas_qk_norm_rope (bf16 weights).
+ * cu_new     device int32 [N + 1]: sequence n brings the token rows cu_new[n] ..
+ *            cu_new[n+1]-1, at most max_new of them (it may bring none). NULL: one token for
+ *            each sequence (T = N, max_new = 1).
+ * kv_len     device int32 [N]: tokens of each sequence with the new ones, which take the
+ *            positions kv_len[n] - count .. kv_len[n] - 1 (so sas_decode_paged takes the
+ *            same kv_len). At most 64 * max_pages and at most max_pos. Without cu_new,
+ *            kv_len 0 is a padding entry: nothing is stored, its q_out and k_out rows are zero.
+ * page_table, max_pages, num_pages   as in sas_decode_paged. The pages that new rows go
+ *            to must belong to one sequence of the call.
+ * k_cache, v_cache  device bf16 [num_pages, Hkv, 64, D] (the new rows are written, the
+ *            others are left as they are).
+ * q_out      device bf16 [T, Hq, D], contiguous (output). k_out: the rotated keys [T,
+ *            Hkv, D], contiguous, for attention over a prompt's own tokens, or NULL.
+ * kpool      device fp32 [num_pages, Hkv, D] or NULL: pages whose last row this call
+ *            writes get their mean key, as sas_pool_pages would write it.
+ * A sequence whose lengths break these terms is flagged and skipped whole; a page id
+ * outside 0 .. num_pages-1 is flagged and the rows for that page are skipped. Rows of
+ * q_out and k_out that belong to no sequence, or to a skipped one, are left as they are.
+ * Outputs must not overlap the inputs. D in {64, 128}, page_size 64.
+ */
+sas_status sas_append_paged(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
+                            int64_t ld_v, const void *q_weight, const void *k_weight,
+                            const float *rope_table, int max_pos, const int32_t *cu_new, int N,
+                            int max_new, int64_t T, const int32_t *kv_len, const int32_t *page_table,
+                            int max_pages, int num_pages, int Hq, int Hkv, int D, int page_size,
+                            float eps, void *q_out, void *k_out, void *k_cache, void *v_cache,
+                            float *kpool, void *stream);
+
+/*
+ * sas_append_paged_q8 - sas_append_paged into 8-bit pages (the layout that
+ * sas_decode_paged_q8 reads).
+ *
+ * k_cache, v_cache  device e4m3 codes [num_pages, Hkv, 64, D].
+ * k_scale, v_scale  device fp32 [num_pages, Hkv]. A page's first row sets its scales
+ *            whatever they held before: the least power of two s (not under 2^-64) with
+ *            |x| <= 448 s for all new values of that page and head. Later rows keep the
+ *            scale if they fit it; else it grows by the same rule and the older rows' codes
+ *            are expressed in it (exactly, but for codes that fall below the normal range).
+ *            Codes are rounded to nearest even. A NaN or an infinity is stored as NaN and
+ *            has no part in the scale. An older scale outside 2^-100 .. 2^120 is flagged
+ *            and the page skipped.
+ * kpool      the mean of the filled page's keys as stored (scale * code).
+ */
+sas_status sas_append_paged_q8(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
+                               int64_t ld_v, const void *q_weight, const void *k_weight,
+                               const float *rope_table, int max_pos, const int32_t *cu_new, int N,
+                               int max_new, int64_t T, const int32_t *kv_len, const int32_t *page_table,
+                               int max_pages, int num_pages, int Hq, int Hkv, int D, int page_size,
+                               float eps, void *q_out, void *k_out, void *k_cache, void *v_cache,
+                               float *k_scale, float *v_scale, float *kpool, void *stream);
+
 /*
  * sas_selftest_bounded_wait - fault injection for the bounded waits, with no
  * GPU fault (no counterpart on the SAS pages: it tests this library's failure

@@ -110,6 +110,40 @@ struct DecodeArgs {
 size_t decode_workspace(int N, int Hq, int Hkv, int D, int K);
 cudaError_t launch_decode(const DecodeArgs& d, void* workspace, cudaStream_t st);
 
+// The same over 8-bit pages (e4m3 codes, one K and one V scale for each page and KV head).
+size_t decode_q8_workspace(int N, int Hq, int Hkv, int K);
+cudaError_t launch_decode_q8(const DecodeArgs& d, const float* k_scale, const float* v_scale, void* workspace,
+                             cudaStream_t st);
+
+// Head norm and position rotation of q and k ([T, H, D] rows, ld values from
+// token to token). Weights of the tensors' type, or both nullptr: rotation
+// only. Position of token row t: positions[t], or t % S without positions.
+struct NormRopeArgs {
+    const void* q; long long ld_q; const void* k; long long ld_k;
+    const void* q_weight; const void* k_weight;
+    const float* table; int max_pos; const int32_t* positions; int S;
+    long long T; int Hq, Hkv; float eps;
+    int* status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, int D, void* q_out, void* k_out, cudaStream_t st);
+size_t norm_rope_bwd_workspace(long long T, int Hq, int Hkv, int D);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, bool bf16, int D, const void* dq_out, const void* dk_out, void* dq,
+                                 void* dk, float* dwq, float* dwk, void* workspace, cudaStream_t st);
+
+// New tokens into a paged cache, with the norm and rotation of q and k. bf16
+// pages, or 8-bit ones when k_scale (and v_scale) is given. q (with q_out),
+// k_out and kpool may be nullptr.
+struct AppendArgs {
+    const void* q; long long ld_q; const void* k; long long ld_k; const void* v; long long ld_v;
+    const void* q_weight; const void* k_weight; const float* table; int max_pos;
+    const int32_t* cu_new; int N, max_new; long long T; const int32_t* kv_len;
+    const int32_t* page_table; int max_pages, num_pages, Hq, Hkv; float eps;
+    void* q_out; void* k_out; void* k_cache; void* v_cache; float* k_scale; float* v_scale; float* kpool;
+    int* status;
+};
+long long append_kv_ctas(const AppendArgs& a);
+cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t st);
+
 // One warp waiting (bounded) on a barrier nothing arrives on: records a timeout in *status.
 cudaError_t launch_bounded_wait_selftest(int* status, cudaStream_t st);
 

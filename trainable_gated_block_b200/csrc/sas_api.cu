@@ -12,6 +12,7 @@
 
 #include "../../include/sas.h"
 #include "launch.h"
+#include "page_rows.h"
 
 namespace {
 
@@ -144,6 +145,79 @@ sas_status attn_bwd_impl(const char* fn, sas_dtype dtype, const void* q, const v
     cudaError_t e = (dtype == SAS_BF16 && D == 128)
                         ? sas::launch_bwd_sm100(b, static_cast<cudaStream_t>(stream))
                         : sas::launch_bwd_simt(b, dtype == SAS_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+// Arguments of a head norm with rotation: row strides, table and weights.
+sas_status check_rows(const char* fn, const char* what, const void* x, int64_t ld, int H, int D, int elem) {
+    if (!x) return fail(SAS_ERR_INVALID_ARG, "%s: null %s", fn, what);
+    if (ld < (int64_t)H * D) return fail(SAS_ERR_INVALID_ARG, "%s: token stride of %s below its %d values", fn, what, H * D);
+    if (!aligned16(x) || ld * elem % 16) return fail(SAS_ERR_INVALID_ARG, "%s: rows of %s not 16-byte aligned", fn, what);
+    return SAS_OK;
+}
+
+sas_status check_rope(const char* fn, const void* q_weight, const void* k_weight, const float* table, int max_pos, int Hq,
+                      int Hkv, int D, float eps) {
+    if (Hq <= 0 || Hkv <= 0 || D <= 0 || max_pos <= 0)
+        return fail(SAS_ERR_INVALID_ARG, "%s: non-positive size (Hq=%d Hkv=%d D=%d max_pos=%d)", fn, Hq, Hkv, D, max_pos);
+    if (D != 64 && D != 128) return fail(SAS_ERR_UNSUPPORTED, "%s: D=%d (only 64 or 128)", fn, D);
+    if (Hq > (1 << 20) || Hkv > (1 << 20)) return fail(SAS_ERR_UNSUPPORTED, "%s: more than 2^20 heads", fn);
+    if (!table || !aligned16(table)) return fail(SAS_ERR_INVALID_ARG, "%s: rope_table null or not 16-byte aligned", fn);
+    if ((q_weight != nullptr) != (k_weight != nullptr))
+        return fail(SAS_ERR_INVALID_ARG, "%s: q_weight and k_weight go together", fn);
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(SAS_ERR_INVALID_ARG, "%s: weights not 16-byte aligned", fn);
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(SAS_ERR_INVALID_ARG, "%s: eps not positive", fn);
+    return SAS_OK;
+}
+
+sas_status check_norm_rope(const char* fn, sas_dtype dtype, const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                           const void* q_weight, const void* k_weight, const float* table, int max_pos,
+                           const int32_t* positions, int S, int64_t T, int Hq, int Hkv, int D, float eps) {
+    if (dtype != SAS_F32 && dtype != SAS_BF16) return fail(SAS_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    sas_status r = check_rope(fn, q_weight, k_weight, table, max_pos, Hq, Hkv, D, eps);
+    if (r != SAS_OK) return r;
+    if (T < 0) return fail(SAS_ERR_INVALID_ARG, "%s: T=%lld", fn, (long long)T);
+    if (T == 0) return SAS_OK;
+    if (!positions && S <= 0) return fail(SAS_ERR_INVALID_ARG, "%s: S=%d without positions", fn, S);
+    if (T > ((1LL << 31) - 1) / (Hq > Hkv ? Hq : Hkv)) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^31", fn);
+    const int elem = dtype == SAS_BF16 ? 2 : 4;
+    if ((r = check_rows(fn, "q", q, ld_q, Hq, D, elem)) != SAS_OK) return r;
+    return check_rows(fn, "k", k, ld_k, Hkv, D, elem);
+}
+
+sas_status append_impl(const char* fn, bool q8, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                       int64_t ld_v, const void* q_weight, const void* k_weight, const float* table, int max_pos,
+                       const int32_t* cu_new, int N, int max_new, int64_t T, const int32_t* kv_len,
+                       const int32_t* page_table, int max_pages, int num_pages, int Hq, int Hkv, int D, int page_size,
+                       float eps, void* q_out, void* k_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       float* kpool, void* stream) {
+    sas_status r = check_rope(fn, q_weight, k_weight, table, max_pos, Hq, Hkv, D, eps);
+    if (r != SAS_OK) return r;
+    if (N < 0 || T < 0 || max_new <= 0 || max_pages <= 0 || num_pages <= 0)
+        return fail(SAS_ERR_INVALID_ARG, "%s: bad size (N=%d T=%lld max_new=%d max_pages=%d num_pages=%d)", fn, N,
+                    (long long)T, max_new, max_pages, num_pages);
+    if (page_size != 64) return fail(SAS_ERR_UNSUPPORTED, "%s: page_size=%d (only 64)", fn, page_size);
+    if (!cu_new && (T != N || max_new != 1))
+        return fail(SAS_ERR_INVALID_ARG, "%s: without cu_new there is one token for each sequence (N=%d T=%lld max_new=%d)",
+                    fn, N, (long long)T, max_new);
+    if (T == 0 || N == 0) return ok();
+    if (!kv_len || !page_table || !k_cache || !v_cache || (q8 && (!k_scale || !v_scale)))
+        return fail(SAS_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if ((q != nullptr) != (q_out != nullptr)) return fail(SAS_ERR_INVALID_ARG, "%s: q and q_out go together", fn);
+    if (q && (r = check_rows(fn, "q", q, ld_q, Hq, D, 2)) != SAS_OK) return r;
+    if ((r = check_rows(fn, "k", k, ld_k, Hkv, D, 2)) != SAS_OK) return r;
+    if ((r = check_rows(fn, "v", v, ld_v, Hkv, D, 2)) != SAS_OK) return r;
+    if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kpool))
+        return fail(SAS_ERR_INVALID_ARG, "%s: tensors not 16-byte aligned", fn);
+    if (T > ((1LL << 31) - 1) / Hq) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^31", fn);
+    if (max_new > (1 << 30)) return fail(SAS_ERR_UNSUPPORTED, "%s: max_new=%d (at most 2^30)", fn, max_new);
+    sas::AppendArgs a{q, ld_q, k, ld_k, v, ld_v, q_weight, k_weight, table, max_pos, cu_new, N, max_new, T, kv_len,
+                      page_table, max_pages, num_pages, Hq, Hkv, eps, q_out, k_out, k_cache, v_cache, k_scale, v_scale,
+                      kpool, nullptr};
+    if (sas::append_kv_ctas(a) > 1LL << 30)
+        return fail(SAS_ERR_UNSUPPORTED, "%s: N x blocks of max_new x Hkv beyond 2^29", fn);
+    if (!(a.status = status_ptr())) return fail(SAS_ERR_CUDA, "%s: no CUDA device", fn);
+    cudaError_t e = sas::launch_append(a, D, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
@@ -418,6 +492,118 @@ sas_status sas_decode_paged(const void* q, const void* k_cache, const void* v_ca
                       idx, cnt, log_gate, sm_scale, o, lse, st};
     cudaError_t e = sas::launch_decode(a, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "sas_decode_paged");
+}
+
+size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K) {
+    if (N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D != 128 || K < 0 || K > 1 << 24) return 0;
+    return sas::decode_q8_workspace(N, Hq, Hkv, K);
+}
+
+sas_status sas_decode_paged_q8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, int num_pages, const int32_t* page_table, int max_pages,
+                               const int32_t* kv_len, int N, int Hq, int Hkv, int D, int page_size, int K,
+                               const int32_t* idx, const int32_t* cnt, const float* log_gate, float sm_scale, void* o,
+                               float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    const char* fn = "sas_decode_paged_q8";
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !kv_len || !cnt || !o || !workspace)
+        return fail(SAS_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (K > 0 && (!idx || !log_gate)) return fail(SAS_ERR_INVALID_ARG, "%s: null idx/log_gate with K > 0", fn);
+    if (N <= 0 || Hq <= 0 || Hkv <= 0 || num_pages <= 0 || max_pages <= 0 || K < 0)
+        return fail(SAS_ERR_INVALID_ARG, "%s: bad size", fn);
+    if (Hq % Hkv) return fail(SAS_ERR_INVALID_ARG, "%s: Hq %% Hkv != 0", fn);
+    if (Hq / Hkv > 8) return fail(SAS_ERR_UNSUPPORTED, "%s: group size %d (at most 8)", fn, Hq / Hkv);
+    if (page_size != 64) return fail(SAS_ERR_UNSUPPORTED, "%s: page_size=%d (only 64)", fn, page_size);
+    if (D != 128) return fail(SAS_ERR_UNSUPPORTED, "%s: D=%d (only 128)", fn, D);
+    if (K > 1 << 24) return fail(SAS_ERR_UNSUPPORTED, "%s: K=%d (at most 2^24)", fn, K);
+    if ((long long)num_pages * Hkv > ((1LL << 31) - 1) / 64)      // TMA row coordinates are int32
+        return fail(SAS_ERR_UNSUPPORTED, "%s: %lld cache rows of a head (at most 2^31 - 1)", fn, (long long)num_pages * Hkv * 64);
+    if ((long long)N * Hkv > (1LL << 31) - 1 || (long long)N * Hq > (1LL << 31) - 1)
+        return fail(SAS_ERR_UNSUPPORTED, "%s: N*Hq=%lld beyond 2^31", fn, (long long)N * Hq);
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o))
+        return fail(SAS_ERR_INVALID_ARG, "%s: tensors not 16-byte aligned", fn);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(SAS_ERR_INVALID_ARG, "%s: workspace not 256-byte aligned", fn);
+    const size_t need = sas_decode_q8_workspace_size(N, Hq, Hkv, D, K);
+    if (ws_bytes < need) return fail(SAS_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (!std::isfinite(sm_scale)) return fail(SAS_ERR_INVALID_ARG, "%s: sm_scale not finite", fn);
+    int* st = status_ptr();
+    if (!st) return fail(SAS_ERR_CUDA, "%s: no CUDA device", fn);
+    sas::DecodeArgs a{q, k_cache, v_cache, num_pages, page_table, max_pages, kv_len, N, Hq, Hkv, D, K,
+                      idx, cnt, log_gate, sm_scale, o, lse, st};
+    cudaError_t e = sas::launch_decode_q8(a, k_scale, v_scale, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+sas_status sas_qk_norm_rope(sas_dtype dtype, const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                            const void* q_weight, const void* k_weight, const float* rope_table, int max_pos,
+                            const int32_t* positions, int S, int64_t T, int Hq, int Hkv, int D, float eps, void* q_out,
+                            void* k_out, void* stream) {
+    const char* fn = "sas_qk_norm_rope";
+    sas_status r = check_norm_rope(fn, dtype, q, ld_q, k, ld_k, q_weight, k_weight, rope_table, max_pos, positions, S, T,
+                                   Hq, Hkv, D, eps);
+    if (r != SAS_OK) return r;
+    if (T == 0) return ok();
+    if (!q_out || !k_out) return fail(SAS_ERR_INVALID_ARG, "%s: null output", fn);
+    if (!aligned16(q_out) || !aligned16(k_out)) return fail(SAS_ERR_INVALID_ARG, "%s: outputs not 16-byte aligned", fn);
+    int* st = status_ptr();
+    if (!st) return fail(SAS_ERR_CUDA, "%s: no CUDA device", fn);
+    sas::NormRopeArgs a{q, ld_q, k, ld_k, q_weight, k_weight, rope_table, max_pos, positions, S, T, Hq, Hkv, eps, st};
+    cudaError_t e = sas::launch_norm_rope(a, dtype == SAS_BF16, D, q_out, k_out, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+size_t sas_qk_norm_rope_bwd_workspace_size(int64_t T, int Hq, int Hkv, int D) {
+    if (T < 0 || Hq <= 0 || Hkv <= 0 || (D != 64 && D != 128)) return 0;
+    return sas::norm_rope_bwd_workspace(T, Hq, Hkv, D);
+}
+
+sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void* dq_out, const void* dk_out, const void* q, int64_t ld_q,
+                                const void* k, int64_t ld_k, const void* q_weight, const void* k_weight,
+                                const float* rope_table, int max_pos, const int32_t* positions, int S, int64_t T, int Hq,
+                                int Hkv, int D, float eps, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                void* workspace, size_t ws_bytes, void* stream) {
+    const char* fn = "sas_qk_norm_rope_bwd";
+    sas_status r = check_norm_rope(fn, dtype, q, ld_q, k, ld_k, q_weight, k_weight, rope_table, max_pos, positions, S, T,
+                                   Hq, Hkv, D, eps);
+    if (r != SAS_OK) return r;
+    if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
+        return fail(SAS_ERR_INVALID_ARG, "%s: weight gradients go with the weights", fn);
+    if (T > 0 && (!dq_out || !dk_out || !dq || !dk)) return fail(SAS_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk))
+        return fail(SAS_ERR_INVALID_ARG, "%s: tensors not 16-byte aligned", fn);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(SAS_ERR_INVALID_ARG, "%s: workspace null or not 256-byte aligned", fn);
+    const size_t need = sas::norm_rope_bwd_workspace(T, Hq, Hkv, D);
+    if (ws_bytes < need) return fail(SAS_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (T == 0 && !q_weight) return ok();
+    int* st = status_ptr();
+    if (!st) return fail(SAS_ERR_CUDA, "%s: no CUDA device", fn);
+    sas::NormRopeArgs a{q, ld_q, k, ld_k, q_weight, k_weight, rope_table, max_pos, positions, S, T, Hq, Hkv, eps, st};
+    cudaError_t e = sas::launch_norm_rope_bwd(a, dtype == SAS_BF16, D, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                                              workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+sas_status sas_append_paged(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                            const void* q_weight, const void* k_weight, const float* rope_table, int max_pos,
+                            const int32_t* cu_new, int N, int max_new, int64_t T, const int32_t* kv_len,
+                            const int32_t* page_table, int max_pages, int num_pages, int Hq, int Hkv, int D,
+                            int page_size, float eps, void* q_out, void* k_out, void* k_cache, void* v_cache,
+                            float* kpool, void* stream) {
+    return append_impl("sas_append_paged", false, q, ld_q, k, ld_k, v, ld_v, q_weight, k_weight, rope_table, max_pos,
+                       cu_new, N, max_new, T, kv_len, page_table, max_pages, num_pages, Hq, Hkv, D, page_size, eps, q_out,
+                       k_out, k_cache, v_cache, nullptr, nullptr, kpool, stream);
+}
+
+sas_status sas_append_paged_q8(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                               const void* q_weight, const void* k_weight, const float* rope_table, int max_pos,
+                               const int32_t* cu_new, int N, int max_new, int64_t T, const int32_t* kv_len,
+                               const int32_t* page_table, int max_pages, int num_pages, int Hq, int Hkv, int D,
+                               int page_size, float eps, void* q_out, void* k_out, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, float* kpool, void* stream) {
+    return append_impl("sas_append_paged_q8", true, q, ld_q, k, ld_k, v, ld_v, q_weight, k_weight, rope_table, max_pos,
+                       cu_new, N, max_new, T, kv_len, page_table, max_pages, num_pages, Hq, Hkv, D, page_size, eps, q_out,
+                       k_out, k_cache, v_cache, k_scale, v_scale, kpool, stream);
 }
 
 sas_status sas_selftest_bounded_wait(void* stream) {

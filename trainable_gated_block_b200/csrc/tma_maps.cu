@@ -1,6 +1,7 @@
-// Tensor maps for TMA loads of [rows, H, D] bf16 tensors (q, k, v, dO).
+// Tensor maps for TMA loads of [rows, H, D] bf16 tensors (q, k, v, dO) and of rows of 8-bit pages.
 #include <cudaTypedefs.h>
 
+#include "byte_map.h"
 #include "launch.h"
 #include "sm100.cuh"
 
@@ -31,6 +32,20 @@ bool make_head_map(CUtensorMap* map, const void* base, long long rows, int H, in
     cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// [rows, 128] bytes viewed as 3-D (128, 1, rows); 128 x 1 x box_rows boxes, 128B swizzle.
+bool make_byte_map(CUtensorMap* map, const void* base, long long rows, int box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {128, 1, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {128, 128};
+    cuuint32_t box[3] = {128, 1, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;

@@ -23,6 +23,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes); must match include/sas.h
 SIGNATURES = {
@@ -49,6 +50,17 @@ SIGNATURES = {
                               _P, _P, _P, _F, _P, _P, _P, _Z, _P]),
     "sas_decode_paged_noalloc": (_I, [_P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I,
                                       _P, _P, _P, _F, _P, _P, _P]),
+    "sas_decode_q8_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "sas_decode_paged_q8": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                                 _P, _P, _P, _F, _P, _P, _P, _Z, _P]),
+    "sas_qk_norm_rope": (_I, [_I, _P, _L, _P, _L, _P, _P, _P, _I, _P, _I, _L, _I, _I, _I, _F, _P, _P, _P]),
+    "sas_qk_norm_rope_bwd_workspace_size": (_Z, [_L, _I, _I, _I]),
+    "sas_qk_norm_rope_bwd": (_I, [_I, _P, _P, _P, _L, _P, _L, _P, _P, _P, _I, _P, _I, _L, _I, _I, _I, _F,
+                                  _P, _P, _P, _P, _P, _Z, _P]),
+    "sas_append_paged": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _P, _I, _I, _L, _P, _P, _I, _I, _I, _I, _I,
+                              _I, _F, _P, _P, _P, _P, _P, _P]),
+    "sas_append_paged_q8": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _P, _I, _I, _L, _P, _P, _I, _I, _I, _I, _I,
+                                 _I, _F, _P, _P, _P, _P, _P, _P, _P, _P]),
     "sas_selftest_bounded_wait": (_I, [_P]),
 }
 
@@ -325,3 +337,220 @@ def decode_paged(q, k_cache, v_cache, page_table, kv_len, idx, cnt, log_gate, sm
                                   _ptr(idx), _ptr(cnt), _ptr(log_gate), sm_scale, _ptr(o), _ptr(lse),
                                   _ptr(workspace), workspace.numel(), _stream()))
     return o, lse
+
+
+def decode_q8_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, K: int) -> int:
+    return int(lib().sas_decode_q8_workspace_size(N, Hq, Hkv, D, K))
+
+
+def _expect(name, t, dtype, shape):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_current_device(*ts):
+    """Every tensor on the current CUDA device, whose stream the call goes to."""
+    for t in ts:
+        if t is not None and t.get_device() < 0:
+            raise ValueError("tensors must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _token_rows(name, t, T: int, H: int, D: int) -> int:
+    """Token stride of [T,H,D] or [B,S,H,D] rows whose heads are contiguous within a token."""
+    st = t.stride()
+    if st[-1] != 1 or (H > 1 and st[-2] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:
+        return H * D
+    if t.dim() == 3:
+        return st[0]
+    B, S = t.shape[:2]
+    if S == 1:
+        return st[0]
+    if B > 1 and st[0] != S * st[1]:
+        raise ValueError(f"{name}: token rows must lie at one stride")
+    return st[1]
+
+
+def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, sm_scale=None,
+                    page_size: int = 64, workspace=None, with_lse: bool = True):
+    """Paged decode over 8-bit pages: caches [P,Hkv,64,D] float8_e4m3fn, scales [P,Hkv] fp32 (a key is
+    k_scale * code). Other arguments as in decode_paged; kv_len 0 is a padding entry (o 0, lse -inf).
+    Returns o [N,Hq,D] and lse [N,Hq] (or None)."""
+    N, Hq, D = q.shape
+    P, Hkv = k_cache.shape[:2]
+    K = idx.shape[-1]
+    f8 = torch.float8_e4m3fn
+    _expect("q", q, torch.bfloat16, (N, Hq, D))
+    _expect("k_cache", k_cache, f8, (P, Hkv, page_size, D))
+    _expect("v_cache", v_cache, f8, (P, Hkv, page_size, D))
+    _expect("k_scale", k_scale, torch.float32, (P, Hkv))
+    _expect("v_scale", v_scale, torch.float32, (P, Hkv))
+    _expect("page_table", page_table, torch.int32, (N, page_table.shape[-1]))
+    _expect("kv_len", kv_len, torch.int32, (N,))
+    _expect("idx", idx, torch.int32, (N, Hkv, K))
+    _expect("cnt", cnt, torch.int32, (N, Hkv))
+    _expect("log_gate", log_gate, torch.float32, (N, Hkv, K))
+    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, workspace)
+    sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
+    o = torch.empty_like(q)
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+    if N == 0:
+        return o, lse
+    if workspace is None:
+        workspace = torch.empty(max(decode_q8_workspace_bytes(N, Hq, Hkv, D, K), 256), dtype=torch.uint8,
+                                device=q.device)
+    _check(lib().sas_decode_paged_q8(_addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), P,
+                                     _addr(page_table), page_table.shape[1], _addr(kv_len), N, Hq, Hkv, D, page_size,
+                                     K, _addr(idx), _addr(cnt), _addr(log_gate), sm_scale, _addr(o), _addr(lse),
+                                     _addr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+    return o, lse
+
+
+def rope_table(max_pos: int, D: int, base: float = 1e6, device="cuda"):
+    """Rotation table [max_pos, D] fp32 for the calls below: D/2 cosines, then D/2 sines, of the angles
+    p * base^(-2i/D), taken in 64 bits. Any other table of this layout (scaled frequencies) serves too."""
+    inv = base ** (-torch.arange(0, D, 2, dtype=torch.float64, device=device) / D)
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), dim=1).float()
+
+
+def _qk_args(q, k, table, q_weight, k_weight, positions):
+    """Checks shared by qk_norm_rope and its gradient; T, S, Hq, Hkv, D and the token strides."""
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"q and k must be [T,H,D] or [B,S,H,D] with the same tokens, got {tuple(q.shape)}, {tuple(k.shape)}")
+    if k.dtype is not q.dtype:
+        raise TypeError(f"q and k must have one dtype, got {q.dtype} and {k.dtype}")
+    Hq, D = q.shape[-2:]
+    Hkv = k.shape[-2]
+    T = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    S = q.shape[-3]
+    _expect("table", table, torch.float32, (table.shape[0], D))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if q_weight is not None:
+        _expect("q_weight", q_weight, q.dtype, (D,))
+        _expect("k_weight", k_weight, q.dtype, (D,))
+    if positions is not None:
+        _expect("positions", positions, torch.int32, q.shape[:-2])
+    elif S > table.shape[0]:
+        raise ValueError(f"{S} positions, the table has {table.shape[0]}")
+    return T, S, Hq, Hkv, D, _token_rows("q", q, T, Hq, D), _token_rows("k", k, T, Hkv, D)
+
+
+def qk_norm_rope(q, k, table, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6):
+    """Per-head RMS norm and rotary position embedding of queries and keys in one pass.
+
+    q [B,S,Hq,D] or [T,Hq,D], k likewise, bf16 or fp32; token rows may be strided (parts of a fused
+    projection's output). Weights [D] of the same dtype (both None: rotation only); table from rope_table;
+    positions int32 of the token shape, or None: 0..S-1 in each sequence (3-D: one sequence).
+    Returns contiguous q and k, as attn_fwd takes them."""
+    T, S, Hq, Hkv, D, ld_q, ld_k = _qk_args(q, k, table, q_weight, k_weight, positions)
+    code = _dtype_code(q)
+    _on_current_device(q, k, table, q_weight, k_weight, positions)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+    _check(lib().sas_qk_norm_rope(code, _addr(q), ld_q, _addr(k), ld_k, _addr(q_weight), _addr(k_weight),
+                                  _addr(table), table.shape[0], _addr(positions), S, T, Hq, Hkv, D, eps,
+                                  _addr(q_out), _addr(k_out), _stream()))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
+                     workspace=None):
+    """Gradients of qk_norm_rope: dq_out, dk_out (contiguous) are those of its outputs, the other arguments
+    its inputs. Returns dq, dk (input dtype, contiguous) and the weights' gradients in fp32 (None without)."""
+    T, S, Hq, Hkv, D, ld_q, ld_k = _qk_args(q, k, table, q_weight, k_weight, positions)
+    code = _dtype_code(q)
+    _expect("dq_out", dq_out, q.dtype, q.shape)
+    _expect("dk_out", dk_out, q.dtype, k.shape)
+    _on_current_device(q, k, dq_out, dk_out, table, q_weight, k_weight, positions, workspace)
+    dev = q.device
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq = torch.empty(D, dtype=torch.float32, device=dev)
+        dwk = torch.empty(D, dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = int(lib().sas_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _check(lib().sas_qk_norm_rope_bwd(code, _addr(dq_out), _addr(dk_out), _addr(q), ld_q, _addr(k), ld_k,
+                                      _addr(q_weight), _addr(k_weight), _addr(table), table.shape[0],
+                                      _addr(positions), S, T, Hq, Hkv, D, eps, _addr(dq), _addr(dk), _addr(dwq),
+                                      _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream()))
+    return dq, dk, dwq, dwk
+
+
+def _append(q8, q, k, v, table, k_cache, v_cache, scales, page_table, kv_len, q_weight, k_weight, cu_new, max_new, eps,
+            kpool, with_k, page_size):
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    P = k_cache.shape[0]
+    N = kv_len.shape[0]
+    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.shape != (T, H, D):
+            raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+    dt = torch.float8_e4m3fn if q8 else torch.bfloat16
+    _expect("table", table, torch.float32, (table.shape[0], D))
+    _expect("k_cache", k_cache, dt, (P, Hkv, page_size, D))
+    _expect("v_cache", v_cache, dt, (P, Hkv, page_size, D))
+    for name, t in zip(("k_scale", "v_scale"), scales):
+        _expect(name, t, torch.float32, (P, Hkv))
+    _expect("page_table", page_table, torch.int32, (N, page_table.shape[-1]))
+    _expect("kv_len", kv_len, torch.int32, (N,))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if q_weight is not None:
+        _expect("q_weight", q_weight, torch.bfloat16, (D,))
+        _expect("k_weight", k_weight, torch.bfloat16, (D,))
+    if cu_new is not None:
+        _expect("cu_new", cu_new, torch.int32, (N + 1,))
+    if kpool is not None:
+        _expect("kpool", kpool, torch.float32, (P, Hkv, D))
+    ld_q, ld_k, ld_v = _token_rows("q", q, T, Hq, D), _token_rows("k", k, T, Hkv, D), _token_rows("v", v, T, Hkv, D)
+    _on_current_device(q, k, v, table, k_cache, v_cache, *scales, page_table, kv_len, q_weight, k_weight, cu_new, kpool)
+    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device) if with_k else None
+    fn = lib().sas_append_paged_q8 if q8 else lib().sas_append_paged
+    _check(fn(_addr(q), ld_q, _addr(k), ld_k, _addr(v), ld_v, _addr(q_weight), _addr(k_weight), _addr(table),
+              table.shape[0], _addr(cu_new), N, max_new, T, _addr(kv_len), _addr(page_table), page_table.shape[1], P,
+              Hq, Hkv, D, page_size, eps, _addr(q_out), _addr(k_out), _addr(k_cache), _addr(v_cache),
+              *map(_addr, scales), _addr(kpool), _stream()))
+    return (q_out, k_out) if with_k else q_out
+
+
+def append_paged(q, k, v, table, k_cache, v_cache, page_table, kv_len, q_weight=None, k_weight=None, cu_new=None,
+                 max_new: int = 1, eps: float = 1e-6, kpool=None, with_k: bool = False, page_size: int = 64):
+    """New tokens into a paged KV cache [P,Hkv,64,D], with the norm and rotation of qk_norm_rope on the way.
+
+    q [T,Hq,D], k, v [T,Hkv,D] bf16 (token rows may be strided). kv_len [N] counts the new tokens. One token
+    for each sequence (T = N; kv_len 0: a padding entry), or with cu_new int32 [N+1] the rows
+    cu_new[n]..cu_new[n+1]-1 of each, at most max_new. kpool [P,Hkv,D]: filled pages get their mean key.
+    Returns the rotated q [T,Hq,D]; with_k: q and the rotated k [T,Hkv,D]."""
+    return _append(False, q, k, v, table, k_cache, v_cache, (), page_table, kv_len, q_weight, k_weight, cu_new,
+                   max_new, eps, kpool, with_k, page_size)
+
+
+def append_paged_q8(q, k, v, table, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, q_weight=None,
+                    k_weight=None, cu_new=None, max_new: int = 1, eps: float = 1e-6, kpool=None, with_k: bool = False,
+                    page_size: int = 64):
+    """append_paged into 8-bit pages: caches float8_e4m3fn, k_scale, v_scale [P,Hkv] fp32 (set by a page's
+    first row, grown where later rows need it)."""
+    return _append(True, q, k, v, table, k_cache, v_cache, (k_scale, v_scale), page_table, kv_len, q_weight,
+                   k_weight, cu_new, max_new, eps, kpool, with_k, page_size)
