@@ -107,6 +107,26 @@ def test_many_sequences_share_the_ctas():
     _check(_run(x), _ref(x))
 
 
+def test_enough_slots_for_the_many_warp_kernel():
+    """N Hkv (K + 1) slots above ten for each of ten warps on every SM; the sequences share pages."""
+    N, Hq, Hkv, K = 64, 16, 8, 30
+    x = _make([64 * 3 + 1] * N, Hq, Hkv, K, seed=20)
+    g = torch.Generator().manual_seed(21)
+    P, blocks = x["k_cache"].shape[0], [int(b) for b in torch.randint(0, 45, (N,), generator=g)]
+    x["page_table"] = torch.randint(0, P, (N, 45), generator=g, dtype=torch.int32)
+    x["kv_len"] = torch.tensor([64 * b + 1 + 7 * (i % 9) for i, b in enumerate(blocks)], dtype=torch.int32)
+    for n, b in enumerate(blocks):
+        c = min(K, b)
+        x["cnt"][n] = c
+        x["idx"][n], x["log_gate"][n] = -1, -math.inf
+        for h in range(Hkv):
+            x["idx"][n, h, :c] = torch.randperm(b, generator=g)[:c].sort().values.to(torch.int32)
+            x["log_gate"][n, h, :c] = -torch.rand(c, generator=g) * 4
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert N * Hkv * (K + 1) >= 10 * 10 * sms
+    _check(_run(x), _ref(x))
+
+
 def test_all_history_of_a_long_sequence():
     x = _make([64 * 300 + 5], 8, 2, 300, seed=5)
     _check(_run(x, sm_scale=0.03), _ref(x, 0.03))

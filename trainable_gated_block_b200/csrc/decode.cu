@@ -29,7 +29,6 @@
 // per-block instruction count low enough that the math hides under the
 // page reads.
 #include "common.cuh"
-#include "decode_split.cuh"
 #include "launch.h"
 #include "sm100.cuh"
 
@@ -38,6 +37,7 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kD = 128;
 constexpr int kWarps = 3;                          // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;        // + one producer warp
 constexpr int kStages = 2 * kWarps;                // warp w owns stages w and w + kWarps
@@ -71,6 +71,12 @@ struct Params {
     float* part_ml;         // [N * Hq, nslot, 2]
     int* status;
 };
+
+// CTA c owns block slots [c V / grid, (c + 1) V / grid); cta_of is its inverse.
+__host__ __device__ __forceinline__ long long slot_begin(long long c, long long V, int grid) { return c * V / grid; }
+__host__ __device__ __forceinline__ int cta_of(long long s, long long V, int grid) {
+    return (int)(((s + 1) * grid - 1) / V);
+}
 
 struct ItemInfo {
     int n, h, L, c, n_sel;
@@ -408,6 +414,52 @@ decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     if (cur_item >= 0) flush();
 }
 
+__global__ void __launch_bounds__(kD)
+decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int nslot, int Hq, int Hkv,
+                      int G, int K, long long V, int grid, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+    // launched as a programmatic dependent of decode_kernel: its blocks may be
+    // resident before the decode grid ends; wait for that grid's writes here
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long row = blockIdx.x;          // n * Hq + hq
+    const int d = threadIdx.x;
+    const long long n = row / Hq;
+    const int hq = (int)(row % Hq);
+    const long long item = n * Hkv + hq / G;
+    const long long s0 = item * (K + 1);
+    const int nsl = cta_of(s0 + K, V, grid) - cta_of(s0, V, grid) + 1;
+    const float* ml = part_ml + row * nslot * 2;
+    float M = -INFINITY;
+    for (int s = 0; s < nsl; ++s) M = fmaxf(M, ml[2 * s]);
+    float Lsum = 0.f, acc = 0.f;
+    if (M != -INFINITY) {
+        for (int s = 0; s < nsl; ++s) {
+            const float w = exp2f(ml[2 * s] - M);     // 0 for empty partials (m = -inf)
+            Lsum = fmaf(ml[2 * s + 1], w, Lsum);
+            acc = fmaf(part_o[(row * nslot + s) * kD + d], w, acc);
+        }
+    }
+    o[row * kD + d] = __float2bfloat16_rn(acc / Lsum);
+    if (lse != nullptr && d == 0) lse[row] = (M + log2f(Lsum)) * kLn2;
+}
+
+struct Layout {
+    long long V;
+    int grid, nslot;
+};
+Layout layout(int N, int Hkv, int K) {
+    Layout r;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 148;
+    r.V = (long long)N * Hkv * (K + 1);
+    r.grid = (int)(r.V < sms ? r.V : sms);
+    if (r.grid < 1) r.grid = 1;
+    const long long mn = r.V / r.grid;                       // shortest CTA range
+    const long long span = (K + 1 + mn - 1) / mn + 1;        // CTAs one item's slots can touch
+    r.nslot = (int)(span < r.grid ? span : r.grid);
+    return r;
+}
+
 }  // namespace
 
 size_t decode_workspace(int N, int Hq, int Hkv, int D, int K) {
@@ -467,7 +519,7 @@ cudaError_t launch_decode(const DecodeArgs& a, void* workspace, cudaStream_t st)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, decode_combine_kernel, (const float*)part_o, (const float*)part_ml, lay.nslot, a.Hq,
-                           a.Hkv, G, a.K, lay.V, lay.grid, (__nv_bfloat16*)a.o, a.lse, NAN);
+                           a.Hkv, G, a.K, lay.V, lay.grid, (__nv_bfloat16*)a.o, a.lse);
     if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();

@@ -12,22 +12,32 @@
 // it), the weights are rounded to fp16 (2^-11 relative); logits, sums and
 // accumulators are fp32.
 //
-// HBM-bound, split as in decode_split.cuh: one persistent CTA per SM streams
-// its share of the kept (page, KV head) tiles, 8 KiB of K and 8 KiB of V, by
-// TMA into a ring of twelve stages. Consumer warp w takes every fourth
-// block and does it whole on mma.sync m16n8k16 with keys (or value dimensions) as
-// the 16 rows and the up to 8 query heads of the group as the 8 columns:
+// HBM-bound design. The kept blocks of all (sequence, KV head) items lie end to
+// end, K + 1 slots each, cut into one contiguous range for each warp of the
+// device. A warp streams its range on its own: its lanes resolve 32 slots at a
+// time (selection entry, page, gate, scales), lane 0 copies the (page, head)
+// tiles, 8 KiB of K and 8 KiB of V, by TMA into the warp's ring, and the warp
+// does each block on mma.sync m16n8k16 with keys (or value dimensions) as the
+// 16 rows and the up to 8 query heads of the group as the 8 columns:
 //   S^T = K Q^T : A from ldmatrix over byte pairs. A lane gets four neighbouring
 //       dimensions of a key; the first two serve as the lane's low k pair, the
 //       others as its high pair, and Q is loaded in the same order.
 //   O^T = V^T P^T : A from ldmatrix.trans over byte pairs, which are two
 //       neighbouring dimensions of a key: the even ones become rows 0..7 of the
 //       tile, the odd ones rows 8..15. P^T comes from S^T by movmatrix.
+// Nothing in the CTA waits for another warp: when a warp leaves an item it writes
+// its state (m, l, o) as one of the item's partials, and a combine kernel joins them.
+//
+// Measured on one B200 (32/8 heads): eight 64k sequences with all history 171.7 us,
+// 6.26 TB/s of codes; 64 sequences at 8k-64k, K = 32: 55.6 us, 4.9 TB/s, of which
+// 8 us are the latency of a call that has one block for each warp (launch, the
+// chain selection entry -> page -> tile, one block's math, the combine). A
+// variant with a producer warp, consumers that meet at each item's end and
+// one exp2f for each logit took 237 and 81.6 us: its math did not keep up.
 #include <cuda_fp16.h>
 
 #include "byte_map.h"
 #include "common.cuh"
-#include "decode_split.cuh"
 #include "launch.h"
 #include "page_rows.h"
 #include "sm100.cuh"
@@ -37,19 +47,31 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 4;                          // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;        // + one producer warp
-constexpr int kStages = 3 * kWarps;                // warp w owns stages w, w + kWarps, w + 2 kWarps
+constexpr int kD = 128;
 constexpr uint32_t kTileBytes = 64 * 128;          // one (page, head) tile of K or V: 64 rows of 128 codes
 constexpr int kShortRows = 8;                      // short box (one 128-byte swizzle period) for a partial block
 constexpr uint32_t kShortBytes = kShortRows * 128;
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kOffMo = kStages * kStageBytes;                 // merge scratch: o [warp][8][D]
-constexpr uint32_t kOffMl = kOffMo + kWarps * 8 * kD * 4;          // merge scratch: m, l [warp][8][2]
-constexpr uint32_t kOffMeta = kOffMl + kWarps * 8 * 2 * 4;         // per stage: bias, valid keys, ks, 1 / vs
-constexpr uint32_t kOffBar = kOffMeta + kStages * 16;
-constexpr uint32_t kSmem = kOffBar + 2 * kStages * 8 + 16 + 1024;  // + alignment slack
-static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+struct Block {              // a resolved block of a warp's stream
+    int row0;               // first cache row of its tile
+    int tokens;             // rows to copy; 0: nothing to read
+    int item;
+    int nvalid;             // rows to attend: tokens, or 0 when the scales are out of range
+    float bias;             // gate + log2(vs), log2 units
+    float ks, inv_vs;
+    int pad;
+};
+constexpr int kList = 64;                           // two batches of a warp
+
+// kWarps warps of one CTA per SM, kDepth ring stages each, and their shared memory.
+template <int kWarps, int kDepth>
+struct Shape {
+    static constexpr uint32_t kOffList = kWarps * kDepth * kStageBytes;
+    static constexpr uint32_t kOffBar = kOffList + kWarps * kList * sizeof(Block);
+    static constexpr uint32_t kOffAbort = kOffBar + kWarps * kDepth * 8;
+    static constexpr uint32_t kSmem = kOffAbort + kWarps * 4 + 1024;       // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
 
 struct Params {
     const __nv_bfloat16* q;
@@ -65,44 +87,30 @@ struct Params {
     const float* log_gate;
     float qscale;           // sm_scale * log2(e)
     long long V;            // n_items * (K + 1) block slots
-    int grid;
+    int ranges;
     int nslot;              // partial slots per query head
     float* part_o;          // [N * Hq, nslot, D]
     float* part_ml;         // [N * Hq, nslot, 2]
     int* status;
 };
 
-struct ItemInfo {
-    int n, h, L, c, n_sel;
-    bool ok;
-};
-__device__ __forceinline__ ItemInfo item_info(const Params& p, int item, bool flag) {
-    ItemInfo r;
-    r.n = item / p.Hkv;
-    r.h = item % p.Hkv;
-    r.L = p.kv_len[r.n];
-    r.ok = r.L >= 1 && r.L <= (long long)p.max_pages * kBlock;
-    r.c = r.ok ? (r.L - 1) / kBlock : 0;
-    r.n_sel = 0;
-    if (!r.ok) {
-        if (r.L != 0 && flag) flag_status(p.status, kStatusBadData);     // 0: a padding entry
-        return r;
-    }
-    const int n_sel = p.cnt[item], hi = min(p.K, r.c);
-    r.n_sel = max(0, min(n_sel, hi));
-    if (r.n_sel != n_sel && flag) flag_status(p.status, kStatusBadData);
-    return r;
+// Range r owns block slots [r V / ranges, (r + 1) V / ranges); range_of is its inverse.
+__host__ __device__ __forceinline__ long long range_begin(long long r, long long V, int ranges) { return r * V / ranges; }
+__host__ __device__ __forceinline__ int range_of(long long s, long long V, int ranges) {
+    return (int)(((s + 1) * ranges - 1) / V);
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -132,263 +140,235 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// A block slot: whether it holds a kept or current block, that block's tile, and
+// its gate and scales as loaded (finish() comes after the tile's copy is under way).
+struct Slot {
+    bool use;
+    int row0, tokens, item;
+    float gate, ks, vs;
+};
+__device__ __forceinline__ Slot resolve(const Params& p, long long v) {
+    Slot r;
+    r.use = false;
+    r.row0 = r.tokens = 0;
+    r.gate = 0.f;
+    r.ks = r.vs = 1.f;
+    const int Kp1 = p.K + 1;
+    const int t = (int)(v % Kp1);
+    r.item = (int)(v / Kp1);
+    const int n = r.item / p.Hkv, h = r.item % p.Hkv;
+    // independent loads first: an entry that turns out not to be one is not used
+    const int L = __ldg(p.kv_len + n), cnt = __ldg(p.cnt + r.item);
+    const long long srow = (long long)r.item * p.K + t;
+    int j = t < p.K ? __ldg(p.idx + srow) : -1;
+    const float gate = t < p.K ? __ldg(p.log_gate + srow) : 0.f;
+    if (L < 1 || L > (long long)p.max_pages * kBlock) {
+        if (L != 0) flag_status(p.status, kStatusBadData);       // 0: a padding entry
+        return r;
+    }
+    const int c = (L - 1) / kBlock;
+    const int n_sel = max(0, min(cnt, min(p.K, c)));
+    if (n_sel != cnt) flag_status(p.status, kStatusBadData);
+    if (t > n_sel) return r;
+    r.use = true;
+    const bool cur = t == n_sel;
+    if (cur) j = c;
+    int page = -1;
+    if (j >= 0 && j < c + cur) page = __ldg(p.page_table + (long long)n * p.max_pages + j);   // j <= c < max_pages
+    if (page < 0 || page >= p.num_pages) {
+        flag_status(p.status, kStatusBadData);
+        return r;
+    }
+    r.row0 = (page * p.Hkv + h) * kBlock;                        // < 2^31 (checked on the host)
+    r.tokens = cur ? L - c * kBlock : kBlock;
+    r.gate = cur ? 0.f : gate;
+    r.ks = __ldg(p.k_scale + (long long)page * p.Hkv + h);
+    r.vs = __ldg(p.v_scale + (long long)page * p.Hkv + h);
+    return r;
+}
+__device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b) {
+    const bool ok = scale_ok(r.ks) && scale_ok(r.vs);
+    if (!ok) flag_status(p.status, kStatusBadData);
+    b.nvalid = ok ? r.tokens : 0;
+    b.bias = r.gate * kLog2e + log2f(r.vs);
+    b.ks = r.ks;
+    b.inv_vs = 1.f / r.vs;
+}
+
+template <int kWarps, int kDepth>
+__global__ void __launch_bounds__(kWarps * 32, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_k8, const __grid_constant__ CUtensorMap map_v8, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* mo = reinterpret_cast<float*>(smem + kOffMo);
-    float* ml = reinterpret_cast<float*>(smem + kOffMl);
-    float4* meta = reinterpret_cast<float4*>(smem + kOffMeta);   // bias (log2 units), valid keys, ks, 1 / vs
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
-    uint64_t* empty = full + kStages;
-    int* abort_flag = reinterpret_cast<int*>(empty + kStages);
-    volatile int* abort = abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
-    __syncthreads();
-
-    const long long v0 = slot_begin(blockIdx.x, p.V, p.grid), v1 = slot_begin(blockIdx.x + 1, p.V, p.grid);
-    const int Kp1 = p.K + 1;
     // the combine kernel may be scheduled now (it waits for this grid to finish)
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+    const int range = warp * (int)gridDim.x + (int)blockIdx.x;
+    if (range >= p.ranges) return;
 
-    if (warp == kWarps) {
-        // ----------------------------------------------------------- producer
-        // The 32 lanes resolve 32 block slots at a time (selection entry, page,
-        // gate, scales: dependent loads, done in parallel); lane 0 then issues
-        // the copies of the kept ones in slot order. The next batch is resolved
-        // once the ring is full, while its copies are in flight.
-        if (lane == 0) {
-            prefetch_tensormap(&map_k);
-            prefetch_tensormap(&map_v);
-            prefetch_tensormap(&map_k8);
-            prefetch_tensormap(&map_v8);
-        }
-        struct Slot {
-            bool use;
-            int row0;
-            float4 m;
-        };
-        auto resolve = [&](long long base) {
-            const long long v = base + lane;
-            Slot s{false, -1, make_float4(0.f, 0.f, 1.f, 1.f)};
-            if (v < v1) {
-                const int item = (int)(v / Kp1), t = (int)(v % Kp1);
-                const ItemInfo inf = item_info(p, item, true);
-                if (inf.ok && t <= inf.n_sel) {
-                    s.use = true;
-                    const bool cur = (t == inf.n_sel);
-                    const long long srow = (long long)item * p.K + t;
-                    const int j = cur ? inf.c : p.idx[srow];
-                    int page = -1;
-                    if (j >= 0 && (cur || j < inf.c))
-                        page = p.page_table[(long long)inf.n * p.max_pages + j];   // j < max_pages by kv_len's check
-                    bool ok = page >= 0 && page < p.num_pages;
-                    if (ok) {
-                        const float ks = __ldg(p.k_scale + (long long)page * p.Hkv + inf.h);
-                        const float vs = __ldg(p.v_scale + (long long)page * p.Hkv + inf.h);
-                        ok = scale_ok(ks) && scale_ok(vs);
-                        s.m.x = (cur ? 0.f : p.log_gate[srow] * kLog2e) + log2f(vs);
-                        s.m.z = ks;
-                        s.m.w = 1.f / vs;
-                    }
-                    if (!ok) flag_status(p.status, kStatusBadData);
-                    s.m.y = ok ? (float)(cur ? inf.L - inf.c * kBlock : kBlock) : 0.f;
-                    s.row0 = ok ? (page * p.Hkv + inf.h) * kBlock : -1;   // < 2^31 (checked on the host)
-                }
-            }
-            return s;
-        };
-        uint32_t it = 0;
-        bool ok_run = true;
-        Slot cur = resolve(v0);
-        for (long long base = v0; base < v1 && ok_run; base += 32) {
-            const bool more = base + 32 < v1;
-            Slot nxt{false, -1, make_float4(0.f, 0.f, 1.f, 1.f)};
-            bool resolved = !more;
-            int issued = 0;
-            unsigned todo = __ballot_sync(0xffffffffu, cur.use);
-            while (todo) {
-                const int b = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int rb = __shfl_sync(0xffffffffu, cur.row0, b);
-                float4 mb;
-                mb.x = __shfl_sync(0xffffffffu, cur.m.x, b);
-                mb.y = __shfl_sync(0xffffffffu, cur.m.y, b);
-                mb.z = __shfl_sync(0xffffffffu, cur.m.z, b);
-                mb.w = __shfl_sync(0xffffffffu, cur.m.w, b);
-                if (lane == 0) {
-                    const int st = it % kStages;
-                    if (!mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, abort, p.status)) {
-                        ok_run = false;
-                    } else {
-                        meta[st] = mb;
-                        uint8_t* dst = smem + st * kStageBytes;
-                        const int nv = (int)mb.y;
-                        if (rb >= 0 && nv < kBlock) {
-                            // partial block (the current one): only the 8-row groups holding tokens
-                            const int ng = (nv + kShortRows - 1) / kShortRows;
-                            mbar_expect_tx(&full[st], (uint32_t)ng * 2 * kShortBytes);
-                            for (int g8 = 0; g8 < ng; ++g8) {
-                                tma_load_3d(dst + g8 * kShortBytes, &map_k8, &full[st], 0, 0, rb + g8 * kShortRows);
-                                tma_load_3d(dst + kTileBytes + g8 * kShortBytes, &map_v8, &full[st], 0, 0,
-                                            rb + g8 * kShortRows);
-                            }
-                        } else if (rb >= 0) {
-                            mbar_expect_tx(&full[st], kStageBytes);
-                            tma_load_3d(dst, &map_k, &full[st], 0, 0, rb);
-                            tma_load_3d(dst + kTileBytes, &map_v, &full[st], 0, 0, rb);
-                        } else {
-                            mbar_arrive(&full[st]);
-                        }
-                        ++it;
-                    }
-                }
-                ok_run = __shfl_sync(0xffffffffu, ok_run, 0);
-                if (!ok_run) break;
-                if (!resolved && ++issued == kStages) {
-                    nxt = resolve(base + 32);
-                    resolved = true;
-                }
-            }
-            if (!resolved) nxt = resolve(base + 32);
-            cur = nxt;
-        }
-        if (lane == 0 && *abort) {       // let the copies in flight land before the CTA exits
-            volatile int no_abort = 0;
-            const uint32_t lo = it > (uint32_t)kStages ? it - kStages : 0;
-            for (uint32_t k = lo; k < it; ++k) mbar_wait(&full[k % kStages], (k / kStages) & 1, &no_abort, nullptr);
-        }
-        return;   // the producer takes no part in the consumers' named barrier
+    uint8_t* ring = smem + warp * kDepth * kStageBytes;
+    Block* list = reinterpret_cast<Block*>(smem + Shape<kWarps, kDepth>::kOffList) + warp * kList;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Shape<kWarps, kDepth>::kOffBar) + warp * kDepth;
+    volatile int* abort = reinterpret_cast<int*>(smem + Shape<kWarps, kDepth>::kOffAbort) + warp;
+    if (lane == 0) {
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        for (int s = 0; s < kDepth; ++s) mbar_init(&full[s], 1);
+        *abort = 0;
+        fence_barrier_init();
     }
+    __syncwarp();
 
-    // -------------------------------------------------------------- consumers
+    const long long v1 = range_begin(range + 1, p.V, p.ranges);
+    long long v = range_begin(range, p.V, p.ranges);        // next slot to resolve
+    const int Kp1 = p.K + 1;
+    const int last_item = (int)((v1 - 1) / Kp1);
+    int cur_item = (int)(v / Kp1);
+
     const int grp = lane >> 2, tig = lane & 3;     // mma fragment coordinates
-    const uint32_t s_base = smem_u32(smem);
-    const int lrow = (lane & 7) + (lane & 8);      // ldmatrix: key of this lane's row within 16, and chunk of two
-    const int lchk = lane >> 4;
+    // ldmatrix: this lane's row within 16 keys; chunk c of that row is at lofs ^ (c << 4) (c even; the odd
+    // chunk of the pair goes to the upper lanes)
+    const uint32_t lofs = sw128_offset((lane & 7) + (lane & 8), lane >> 4);
+    const uint32_t ring_s = smem_u32(ring) + lofs;
     uint32_t qb[8][2];          // Q^T as B fragments: 8 k-steps x (dims 4tig, +1 / +2, +3 of the step) of head grp
     float o[8][4];              // O^T: tile mt, dims 16mt + 2grp (+1 in [2], [3]) x heads 2tig, 2tig + 1
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};     // heads 2tig, 2tig + 1: max of y; this lane's part of the sum
-    float qm[2] = {0.f, 0.f};   // sm_scale log2(e) over the query scale of those heads
-    uint32_t blk = 0;           // blocks of this CTA's stream seen so far
-    int cur_item = -1;
-    ItemInfo inf{};
-    bool dead = false;
+    float m[2], l[2];           // heads 2tig, 2tig + 1: max of y; this lane's part of the sum
+    float qm[2];                // sm_scale log2(e) over the query scale of those heads
 
-    auto flush = [&]() {
-        // sum over the lanes that share a head, then every warp's state to shared memory
+    auto start = [&](int item) {
+        const int n = item / p.Hkv, h = item % p.Hkv;
+        const bool real = grp < p.G;
+        const uint2* qrow = reinterpret_cast<const uint2*>(p.q + ((long long)n * p.Hq + h * p.G + (real ? grp : 0)) * kD);
+        uint2 qr[8];
+        float top = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) qr[kk] = real ? __ldg(qrow + 4 * kk + tig) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            const float2 a = bf16x2_to_f32(qr[kk].x), b = bf16x2_to_f32(qr[kk].y);
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e with top 2^e in [2^13, 2^14); 1 for a zero or infinite row
+        const int te = (int)(__float_as_uint(top) >> 23);           // biased exponent of top
+        const int e = te == 0 || te == 255 ? 0 : min(13 + 127 - te, 126);
+        const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            const float2 a = bf16x2_to_f32(qr[kk].x), b = bf16x2_to_f32(qr[kk].y);
+            qb[kk][0] = pack_f16x2(a.x * qs, a.y * qs);
+            qb[kk][1] = pack_f16x2(b.x * qs, b.y * qs);
+        }
+        const float qi = p.qscale * __uint_as_float((uint32_t)(127 - e) << 23);
+        qm[0] = __shfl_sync(0xffffffffu, qi, 8 * tig);
+        qm[1] = __shfl_sync(0xffffffffu, qi, 8 * tig + 4);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    };
+    // row of the item's first query head, at this range's partial slot
+    auto part_row = [&](int item) {
+        const int n = item / p.Hkv, h = item % p.Hkv;
+        return ((long long)n * p.Hq + h * p.G) * p.nslot + (range - range_of((long long)item * Kp1, p.V, p.ranges));
+    };
+    auto write_empty = [&](int item) {
+        if (lane < p.G) {
+            float* ml = p.part_ml + (part_row(item) + (long long)lane * p.nslot) * 2;
+            ml[0] = -INFINITY;
+            ml[1] = 0.f;
+        }
+    };
+    auto write = [&](int item) {
+        const long long row = part_row(item);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
             if (l[e] != l[e]) m[e] = fmaxf(m[e], -1e30f);     // only NaN logits: the row is not an empty one
+            const int g = 2 * tig + e;
+            if (g >= p.G) continue;
+            const long long r = row + (long long)g * p.nslot;
+            if (grp == 0) *reinterpret_cast<float2*>(p.part_ml + r * 2) = make_float2(m[e], l[e]);
+            float* dst = p.part_o + r * kD + 2 * grp;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) *reinterpret_cast<float2*>(dst + 16 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
         }
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float2*>(mo + (warp * 8 + 2 * tig + e) * kD + 16 * mt + 2 * grp) =
-                    make_float2(o[mt][e], o[mt][2 + e]);
-        if (grp == 0) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ml[(warp * 8 + 2 * tig + e) * 2] = m[e];
-                ml[(warp * 8 + 2 * tig + e) * 2 + 1] = l[e];
-            }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        const int slot = (int)blockIdx.x - cta_of((long long)cur_item * Kp1, p.V, p.grid);
-        for (int e = threadIdx.x; e < p.G * kD; e += kWarps * 32) {
-            const int g = e / kD, d = e % kD;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * 8 + g) * 2]);
-            float acc = 0.f, L = 0.f;
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float mw = ml[(w * 8 + g) * 2];
-                    const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-                    acc = fmaf(mo[(w * 8 + g) * kD + d], f, acc);
-                    L = fmaf(ml[(w * 8 + g) * 2 + 1], f, L);
-                }
-            }
-            const long long row = ((long long)inf.n * p.Hq + inf.h * p.G + g) * p.nslot + slot;
-            p.part_o[row * kD + d] = acc;
-            if (d == 0) {
-                p.part_ml[row * 2] = M;
-                p.part_ml[row * 2 + 1] = L;
-            }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
     };
 
-    for (long long v = v0; v < v1; ++v) {
-        const int item = (int)(v / Kp1), t = (int)(v % Kp1);
-        if (item != cur_item) {
-            if (cur_item >= 0) flush();
-            cur_item = item;
-            inf = item_info(p, item, false);
-            const bool real = grp < p.G;
-            const uint2* qrow = reinterpret_cast<const uint2*>(
-                p.q + ((long long)inf.n * p.Hq + inf.h * p.G + (real ? grp : 0)) * kD);
-            uint2 qr[8];
-            float top = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                qr[kk] = real ? __ldg(qrow + 4 * kk + tig) : make_uint2(0u, 0u);
-                const float2 a = bf16x2_to_f32(qr[kk].x), b = bf16x2_to_f32(qr[kk].y);
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+    uint32_t found = 0, issued = 0, done = 0;      // blocks resolved, copied, consumed
+    bool started = false, alive = true;
+    while (true) {
+        // resolve a batch of slots when the ring has nothing more to copy
+        Slot slot;
+        slot.use = false;
+        uint32_t at = 0;
+        if (v < v1 && found == issued && found - done <= kList - 32) {
+            if (v + lane < v1) slot = resolve(p, v + lane);
+            const unsigned mask = __ballot_sync(0xffffffffu, slot.use);
+            at = (found + __popc(mask & ((1u << lane) - 1u))) % kList;
+            if (slot.use) {
+                list[at].row0 = slot.row0;
+                list[at].tokens = slot.tokens;
+                list[at].item = slot.item;
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e with top 2^e in [2^13, 2^14); 1 for a zero or infinite row
-            const int te = (int)(__float_as_uint(top) >> 23);           // biased exponent of top
-            const int e = te == 0 || te == 255 ? 0 : min(13 + 127 - te, 126);
-            const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                const float2 a = bf16x2_to_f32(qr[kk].x), b = bf16x2_to_f32(qr[kk].y);
-                qb[kk][0] = pack_f16x2(a.x * qs, a.y * qs);
-                qb[kk][1] = pack_f16x2(b.x * qs, b.y * qs);
+            found += __popc(mask);
+            v += 32;
+            __syncwarp();
+        }
+        while (issued < found && issued - done < kDepth) {
+            if (lane == 0) {
+                const Block& b = list[issued % kList];
+                const uint32_t st = issued % kDepth;
+                uint8_t* dst = ring + st * kStageBytes;
+                if (b.tokens == kBlock) {
+                    mbar_expect_tx(&full[st], kStageBytes);
+                    tma_load_3d(dst, &map_k, &full[st], 0, 0, b.row0);
+                    tma_load_3d(dst + kTileBytes, &map_v, &full[st], 0, 0, b.row0);
+                } else {
+                    // partial block (the current one): only the 8-row groups holding tokens; none of a skipped one
+                    const int ng = (b.tokens + kShortRows - 1) / kShortRows;
+                    mbar_expect_tx(&full[st], (uint32_t)ng * 2 * kShortBytes);
+                    for (int g8 = 0; g8 < ng; ++g8) {
+                        tma_load_3d(dst + g8 * kShortBytes, &map_k8, &full[st], 0, 0, b.row0 + g8 * kShortRows);
+                        tma_load_3d(dst + kTileBytes + g8 * kShortBytes, &map_v8, &full[st], 0, 0,
+                                    b.row0 + g8 * kShortRows);
+                    }
+                }
             }
-            const float qi = p.qscale * __uint_as_float((uint32_t)(127 - e) << 23);
-            qm[0] = __shfl_sync(0xffffffffu, qi, 8 * tig);
-            qm[1] = __shfl_sync(0xffffffffu, qi, 8 * tig + 4);
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-            m[0] = m[1] = -INFINITY;
-            l[0] = l[1] = 0.f;
+            ++issued;
         }
-        if (!inf.ok || t > inf.n_sel) continue;
-        const uint32_t b = blk++;
-        if (b % kWarps != (uint32_t)warp || dead) continue;      // another warp's block
-        const int st = b % kStages;
-        if (!mbar_wait_warp(&full[st], (b / kStages) & 1, abort, p.status)) {
-            dead = true;              // keep walking the slots so the flush barriers still meet
-            continue;
+        if (slot.use) finish(p, slot, list[at]);
+        __syncwarp();
+        if (done == issued) {
+            if (v < v1) continue;
+            break;                                 // nothing left in this range
         }
-        const float4 md = meta[st];
-        const int nvalid = (int)md.y;
-        if (nvalid > 0) {
-            const uint32_t kt = s_base + st * kStageBytes, vt = kt + kTileBytes;
+        const Block b = list[done % kList];
+        const uint32_t st = done % kDepth;
+        if (!started || b.item != cur_item) {
+            if (started) write(cur_item++);
+            for (; cur_item < b.item; ++cur_item) write_empty(cur_item);
+            start(b.item);
+            started = true;
+        }
+        if (!mbar_wait_warp(&full[st], (done / kDepth) & 1, abort, p.status)) {
+            alive = false;
+            break;
+        }
+        if (b.nvalid > 0) {
+            const uint32_t kt = ring_s + st * kStageBytes, vt = kt + kTileBytes;
             float s[4][4];      // S^T: keys 16mt + grp (+8 in [2], [3]) x heads 2tig, 2tig + 1
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+            for (int mt = 0; mt < 4; ++mt) s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
 #pragma unroll
-                for (int kk = 0; kk < 8; kk += 2) {
+            for (int kk = 0; kk < 8; kk += 2) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
                     uint32_t r[4], a0, a1, a2, a3;
-                    ldsm_x4(kt + sw128_offset(16 * mt + lrow, kk + lchk), r);
+                    ldsm_x4((kt ^ (kk << 4)) + mt * 2048, r);
                     codes_f16(r[0], a0, a2);
                     codes_f16(r[1], a1, a3);
                     mma16816(s[mt], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
@@ -397,24 +377,37 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     mma16816(s[mt], a0, a1, a2, a3, qb[kk + 1][0], qb[kk + 1][1]);
                 }
             }
+            const float f[2] = {qm[0] * b.ks, qm[1] * b.ks};
             float bm[2] = {-INFINITY, -INFINITY};
-            const float f[2] = {qm[0] * md.z, qm[1] * md.z};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = 16 * mt + grp + 8 * (e >> 1);
-                    const float y = key < nvalid ? fmaf(s[mt][e], f[e & 1], md.x) : -INFINITY;
-                    s[mt][e] = y;
-                    bm[e & 1] = fmaxf(bm[e & 1], y);
-                }
-            float sc[2], ls[2] = {0.f, 0.f};
+                for (int e = 0; e < 4; ++e) s[mt][e] = fmaf(s[mt][e], f[e & 1], b.bias);
+            if (b.nvalid < kBlock) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (16 * mt + grp + 8 * (e >> 1) >= b.nvalid) s[mt][e] = -INFINITY;
+                // rows past the sequence end are zeroed: their weight is 0, but whatever
+                // the page holds there must not reach O as 0 * NaN
+                uint8_t* vrow = ring + st * kStageBytes + kTileBytes;
+                for (int e = b.nvalid * 8 + lane; e < kBlock * 8; e += 32)
+                    *reinterpret_cast<uint4*>(vrow + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) bm[e] = max3(bm[e], s[mt][e], s[mt][e + 2]);
+            float sc[2], mu[2], ls[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], x));
                 const float mn = fmaxf(m[e], bm[e]);
-                sc[e] = mn == -INFINITY ? 1.f : exp2f(m[e] - mn);
+                mu[e] = mn == -INFINITY ? 0.f : mn;              // a block of closed gates: 2^(-inf - 0) = 0
+                sc[e] = fast_exp2(m[e] - mu[e]);
                 m[e] = mn;
             }
             uint32_t pb[4][2];          // P^T as B fragments
@@ -422,33 +415,26 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[mt][e] = s[mt][e] == -INFINITY ? 0.f : exp2f(s[mt][e] - m[e & 1]);
+                    s[mt][e] = fast_exp2(s[mt][e] - mu[e & 1]);
                     ls[e & 1] += s[mt][e];
                 }
                 pb[mt][0] = transpose8x8(pack_f16x2(s[mt][0], s[mt][1]));
                 pb[mt][1] = transpose8x8(pack_f16x2(s[mt][2], s[mt][3]));
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], sc[e], ls[e] * md.w);
+            for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], sc[e], ls[e] * b.inv_vs);
+            if (__any_sync(0xffffffffu, sc[0] != 1.f || sc[1] != 1.f)) {     // a maximum grew
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
+                for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][e] *= sc[e & 1];
-            if (nvalid < kBlock) {
-                // rows past the sequence end (the current block) are zeroed: their weight
-                // is 0, but whatever the page holds there must not reach O as 0 * NaN
-                uint8_t* vrow = smem + st * kStageBytes + kTileBytes;
-                for (int e = nvalid * 8 + lane; e < kBlock * 8; e += 32)
-                    *reinterpret_cast<uint4*>(vrow + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();     // ordered before the stage's next TMA refill
-                __syncwarp();
+                    for (int e = 0; e < 4; ++e) o[mt][e] *= sc[e & 1];
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                 for (int mt = 0; mt < 8; mt += 2) {
                     uint32_t r[4], a0, a1, a2, a3;
-                    ldsm_x4_t(vt + sw128_offset(16 * kk + lrow, mt + lchk), r);
+                    ldsm_x4_t((vt ^ (mt << 4)) + kk * 2048, r);
                     codes_f16(__byte_perm(r[0], 0u, 0x3120), a0, a1);
                     codes_f16(__byte_perm(r[1], 0u, 0x3120), a2, a3);
                     mma16816(o[mt], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
@@ -457,10 +443,127 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     mma16816(o[mt + 1], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
                 }
         }
+        fence_proxy_async_smem();     // this stage's reads and zeroes before its next copy
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
+        ++done;
     }
-    if (cur_item >= 0) flush();
+    if (!alive) {                     // let the copies in flight land before the CTA exits
+        volatile int no_abort = 0;
+        for (uint32_t k = done; k < issued; ++k) mbar_wait(&full[k % kDepth], (k / kDepth) & 1, &no_abort, nullptr);
+    }
+    if (started) write(cur_item++);
+    for (; cur_item <= last_item; ++cur_item) write_empty(cur_item);
+}
+
+// Joins the partials of one (sequence, query head): kGroups groups of threads
+// take every kGroups-th partial, one thread of a group for each output
+// dimension, and meet in shared memory. Latency is what counts here: a thread
+// has the loads of eight partials in flight. A row without a readable block
+// gets 0 and an lse of -inf.
+template <int kGroups>
+__global__ void __launch_bounds__(kD* kGroups)
+decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int nslot, int Hq, int Hkv,
+                         int G, int K, long long V, int ranges, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+    __shared__ float acc_s[kGroups][kD];
+    __shared__ float2 ml_s[kGroups];
+    // launched as a programmatic dependent of decode_q8_kernel: its blocks may be
+    // resident before that grid ends; wait for its writes here
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long row = blockIdx.x;          // n * Hq + hq
+    const int d = threadIdx.x % kD, grp = threadIdx.x / kD;
+    const long long s0 = (row / Hq * Hkv + row % Hq / G) * (K + 1);
+    const int n = range_of(s0 + K, V, ranges) - range_of(s0, V, ranges) + 1;
+    const float2* ml = reinterpret_cast<const float2*>(part_ml) + row * nslot;
+    const float* po = part_o + row * nslot * kD + d;
+    float M = -INFINITY, L = 0.f, acc = 0.f;
+    for (int base = grp; base < n; base += 8 * kGroups) {
+        float2 w[8];
+        float x[8];
+        float mx = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int s = base + i * kGroups;
+            w[i] = s < n ? ml[s] : make_float2(-INFINITY, 0.f);
+            x[i] = s < n ? po[(long long)s * kD] : 0.f;    // not written for an empty partial: not used then
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, w[i].x);
+        if (mx == -INFINITY) continue;
+        const float f0 = exp2f(M - mx);
+        L *= f0;
+        acc *= f0;
+        M = mx;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (w[i].x == -INFINITY) continue;
+            const float f = exp2f(w[i].x - M);
+            L = fmaf(w[i].y, f, L);
+            acc = fmaf(x[i], f, acc);
+        }
+    }
+    if (kGroups > 1) {
+        acc_s[grp][d] = acc;
+        if (d == 0) ml_s[grp] = make_float2(M, L);
+        __syncthreads();
+        if (grp) return;
+        float mx = M;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) mx = fmaxf(mx, ml_s[i].x);
+        if (mx != -INFINITY) {
+            const float f0 = exp2f(M - mx);
+            L *= f0;
+            acc *= f0;
+            M = mx;
+#pragma unroll
+            for (int i = 1; i < kGroups; ++i) {
+                if (ml_s[i].x == -INFINITY) continue;
+                const float f = exp2f(ml_s[i].x - M);
+                L = fmaf(ml_s[i].y, f, L);
+                acc = fmaf(acc_s[i][d], f, acc);
+            }
+        }
+    }
+    const bool none = M == -INFINITY;
+    o[row * kD + d] = __float2bfloat16_rn(none ? 0.f : acc / L);
+    if (lse != nullptr && d == 0) lse[row] = none ? M : (M + log2f(L)) * kLn2;
+}
+
+// Ten warps with one stage each hide the math better than four with three, but
+// cut the slots into more ranges, whose lengths differ by one. Measured (32/8
+// heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120 slots 66.3 /
+// 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten slots a
+// range on.
+constexpr int kManyWarps = 10, kFewWarps = 4;
+constexpr int kManySlots = 10;
+
+struct Layout {
+    long long V;
+    bool many;
+    int grid, ranges, nslot;
+};
+Layout layout(int N, int Hkv, int K) {
+    Layout r;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 148;
+    r.V = (long long)N * Hkv * (K + 1);
+    r.many = r.V >= (long long)kManySlots * kManyWarps * sms;
+    r.grid = (int)(r.V < sms ? r.V : sms);
+    const long long most = (long long)sms * (r.many ? kManyWarps : kFewWarps);
+    r.ranges = (int)(r.V < most ? r.V : most);
+    const long long mn = r.V / r.ranges;                     // shortest range
+    const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
+    r.nslot = (int)(span < r.ranges ? span : r.ranges);
+    return r;
+}
+
+template <int kWarps, int kDepth>
+cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params& p, cudaStream_t st) {
+    constexpr int kSmem = (int)Shape<kWarps, kDepth>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<kWarps, kDepth>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    decode_q8_kernel<kWarps, kDepth><<<lay.grid, kWarps * 32, kSmem, st>>>(map[0], map[1], map[2], map[3], p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -477,9 +580,10 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     const Layout lay = layout(a.N, a.Hkv, a.K);
     float* part_o = static_cast<float*>(workspace);
     float* part_ml = part_o + (size_t)a.N * a.Hq * lay.nslot * kD;
-    CUtensorMap mk, mv, mk8, mv8;
-    if (!make_byte_map(&mk, a.k_cache, cache_rows, kBlock) || !make_byte_map(&mv, a.v_cache, cache_rows, kBlock) ||
-        !make_byte_map(&mk8, a.k_cache, cache_rows, kShortRows) || !make_byte_map(&mv8, a.v_cache, cache_rows, kShortRows))
+    CUtensorMap map[4];
+    if (!make_byte_map(&map[0], a.k_cache, cache_rows, kBlock) || !make_byte_map(&map[1], a.v_cache, cache_rows, kBlock) ||
+        !make_byte_map(&map[2], a.k_cache, cache_rows, kShortRows) ||
+        !make_byte_map(&map[3], a.v_cache, cache_rows, kShortRows))
         return cudaErrorInvalidValue;
     Params p;
     p.q = (const __nv_bfloat16*)a.q;
@@ -498,19 +602,17 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     p.log_gate = a.log_gate;
     p.qscale = a.sm_scale * kLog2e;
     p.V = lay.V;
-    p.grid = lay.grid;
+    p.ranges = lay.ranges;
     p.nslot = lay.nslot;
     p.part_o = part_o;
     p.part_ml = part_ml;
     p.status = a.status;
-    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    cudaError_t e = lay.many ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
     if (e != cudaSuccess) return e;
-    decode_q8_kernel<<<lay.grid, kThreads, kSmem, st>>>(mk, mv, mk8, mv8, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // programmatic dependent launch: the combine's blocks are placed while the decode grid drains
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * a.Hq));
-    cfg.blockDim = dim3(kD);
+    cfg.blockDim = dim3(lay.nslot > 8 ? 4 * kD : kD);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -518,8 +620,9 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel, (const float*)part_o, (const float*)part_ml, lay.nslot, a.Hq,
-                           a.Hkv, p.G, a.K, lay.V, lay.grid, (__nv_bfloat16*)a.o, a.lse, 0.f);
+    const auto combine = lay.nslot > 8 ? decode_q8_combine_kernel<4> : decode_q8_combine_kernel<1>;
+    e = cudaLaunchKernelEx(&cfg, combine, (const float*)part_o, (const float*)part_ml, lay.nslot, a.Hq, a.Hkv, p.G, a.K,
+                           lay.V, lay.ranges, (__nv_bfloat16*)a.o, a.lse);
     if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();
