@@ -343,45 +343,62 @@ def decode_q8_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, K: int) -> int:
     return int(lib().sas_decode_q8_workspace_size(N, Hq, Hkv, D, K))
 
 
-def _expect(name, t, dtype, shape):
+_BF16, _F32T, _I32, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def _raw_stream(dev: int) -> int:
+    """torch's current stream on a device, without building a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _expect(name, t, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of this dtype, shape and device; raises on any other."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on the device of the other tensors")
 
 
-def _on_current_device(*ts):
-    """Every tensor on the current CUDA device, whose stream the call goes to."""
-    for t in ts:
-        if t is not None and t.get_device() < 0:
-            raise ValueError("tensors must be CUDA tensors")
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _token_rows(name, t, T: int, H: int, D: int) -> int:
+def _expect_rows(name, t, dtype, shape, dev) -> int:
     """Token stride of [T,H,D] or [B,S,H,D] rows whose heads are contiguous within a token."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
     st = t.stride()
+    H, D = shape[-2:]
     if st[-1] != 1 or (H > 1 and st[-2] != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if T <= 1:
-        return H * D
-    if t.dim() == 3:
-        return st[0]
-    B, S = t.shape[:2]
-    if S == 1:
-        return st[0]
-    if B > 1 and st[0] != S * st[1]:
+    if len(shape) == 3:
+        return st[0] if shape[0] > 1 else H * D
+    B, S = shape[:2]
+    if B > 1 and S > 1 and st[0] != S * st[1]:
         raise ValueError(f"{name}: token rows must lie at one stride")
-    return st[1]
+    return st[1] if S > 1 else st[0] if B > 1 else H * D
+
+
+def _expect_current(dev: int):
+    """The tensors' device must be the current CUDA device, whose stream the call goes to."""
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+
+
+def _workspace(workspace, need: int, dev: int, like):
+    """Address and bytes of the caller's workspace, or of a new one (third, to be kept until the launch)."""
+    if workspace is None:
+        workspace = like.new_empty(max(need, 256), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, sm_scale=None,
@@ -392,30 +409,28 @@ def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, i
     N, Hq, D = q.shape
     P, Hkv = k_cache.shape[:2]
     K = idx.shape[-1]
-    f8 = torch.float8_e4m3fn
-    _expect("q", q, torch.bfloat16, (N, Hq, D))
-    _expect("k_cache", k_cache, f8, (P, Hkv, page_size, D))
-    _expect("v_cache", v_cache, f8, (P, Hkv, page_size, D))
-    _expect("k_scale", k_scale, torch.float32, (P, Hkv))
-    _expect("v_scale", v_scale, torch.float32, (P, Hkv))
-    _expect("page_table", page_table, torch.int32, (N, page_table.shape[-1]))
-    _expect("kv_len", kv_len, torch.int32, (N,))
-    _expect("idx", idx, torch.int32, (N, Hkv, K))
-    _expect("cnt", cnt, torch.int32, (N, Hkv))
-    _expect("log_gate", log_gate, torch.float32, (N, Hkv, K))
-    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, workspace)
+    max_pages = page_table.shape[-1]
+    dev = q.get_device()
+    pages = (P, Hkv, page_size, D)
+    ptrs = (_expect("q", q, _BF16, (N, Hq, D), dev), _expect("k_cache", k_cache, _F8, pages, dev),
+            _expect("v_cache", v_cache, _F8, pages, dev), _expect("k_scale", k_scale, _F32T, (P, Hkv), dev),
+            _expect("v_scale", v_scale, _F32T, (P, Hkv), dev))
+    pt = _expect("page_table", page_table, _I32, (N, max_pages), dev)
+    kv = _expect("kv_len", kv_len, _I32, (N,), dev)
+    sel = (_expect("idx", idx, _I32, (N, Hkv, K), dev), _expect("cnt", cnt, _I32, (N, Hkv), dev),
+           _expect("log_gate", log_gate, _F32T, (N, Hkv, K), dev))
+    _expect_current(dev)
     sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
     o = torch.empty_like(q)
-    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+    lse = q.new_empty((N, Hq), dtype=_F32T) if with_lse else None
     if N == 0:
         return o, lse
-    if workspace is None:
-        workspace = torch.empty(max(decode_q8_workspace_bytes(N, Hq, Hkv, D, K), 256), dtype=torch.uint8,
-                                device=q.device)
-    _check(lib().sas_decode_paged_q8(_addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), P,
-                                     _addr(page_table), page_table.shape[1], _addr(kv_len), N, Hq, Hkv, D, page_size,
-                                     K, _addr(idx), _addr(cnt), _addr(log_gate), sm_scale, _addr(o), _addr(lse),
-                                     _addr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+    L = lib()
+    ws, ws_bytes, workspace = _workspace(workspace, L.sas_decode_q8_workspace_size(N, Hq, Hkv, D, K), dev, q)
+    code = L.sas_decode_paged_q8(*ptrs, P, pt, max_pages, kv, N, Hq, Hkv, D, page_size, K, *sel, sm_scale, o.data_ptr(),
+                                 lse.data_ptr() if with_lse else None, ws, ws_bytes, _raw_stream(dev))
+    if code:
+        _check(code)
     return o, lse
 
 
@@ -427,27 +442,37 @@ def rope_table(max_pos: int, D: int, base: float = 1e6, device="cuda"):
     return torch.cat((ang.cos(), ang.sin()), dim=1).float()
 
 
-def _qk_args(q, k, table, q_weight, k_weight, positions):
-    """Checks shared by qk_norm_rope and its gradient; T, S, Hq, Hkv, D and the token strides."""
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
-        raise ValueError(f"q and k must be [T,H,D] or [B,S,H,D] with the same tokens, got {tuple(q.shape)}, {tuple(k.shape)}")
-    if k.dtype is not q.dtype:
-        raise TypeError(f"q and k must have one dtype, got {q.dtype} and {k.dtype}")
-    Hq, D = q.shape[-2:]
-    Hkv = k.shape[-2]
-    T = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
-    S = q.shape[-3]
-    _expect("table", table, torch.float32, (table.shape[0], D))
-    if (q_weight is None) != (k_weight is None):
+def _weight_ptrs(q_weight, k_weight, dtype, D, dev):
+    if q_weight is None and k_weight is None:
+        return None, None
+    if q_weight is None or k_weight is None:
         raise ValueError("q_weight and k_weight go together")
-    if q_weight is not None:
-        _expect("q_weight", q_weight, q.dtype, (D,))
-        _expect("k_weight", k_weight, q.dtype, (D,))
+    return _expect("q_weight", q_weight, dtype, (D,), dev), _expect("k_weight", k_weight, dtype, (D,), dev)
+
+
+def _qk_args(q, k, table, q_weight, k_weight, positions, eps):
+    """Checks shared by qk_norm_rope and its gradient: the C calls' arguments from the dtype (first) and from
+    q on, and T, Hq, Hkv, D and the device."""
+    qs, ks = q.shape, k.shape
+    n = len(qs)
+    if n not in (3, 4) or len(ks) != n or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
+        raise ValueError(f"q and k must be [T,H,D] or [B,S,H,D] with the same tokens, got {tuple(qs)}, {tuple(ks)}")
+    dtype, dev = q.dtype, q.get_device()
+    Hq, D = qs[-2:]
+    Hkv, S = ks[-2], qs[-3]
+    T = S if n == 3 else S * qs[0]
+    max_pos = table.shape[0]
+    ld_q, ld_k = _expect_rows("q", q, dtype, qs, dev), _expect_rows("k", k, dtype, ks, dev)
+    tab = _expect("table", table, _F32T, (max_pos, D), dev)
+    w = _weight_ptrs(q_weight, k_weight, dtype, D, dev)
+    pos = None
     if positions is not None:
-        _expect("positions", positions, torch.int32, q.shape[:-2])
-    elif S > table.shape[0]:
-        raise ValueError(f"{S} positions, the table has {table.shape[0]}")
-    return T, S, Hq, Hkv, D, _token_rows("q", q, T, Hq, D), _token_rows("k", k, T, Hkv, D)
+        pos = _expect("positions", positions, _I32, qs[:-2], dev)
+    elif S > max_pos:
+        raise ValueError(f"{S} positions, the table has {max_pos}")
+    code = _dtype_code(q)
+    _expect_current(dev)
+    return code, (q.data_ptr(), ld_q, k.data_ptr(), ld_k, *w, tab, max_pos, pos, S, T, Hq, Hkv, D, eps), (T, Hq, Hkv, D, dev)
 
 
 def qk_norm_rope(q, k, table, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6):
@@ -457,14 +482,11 @@ def qk_norm_rope(q, k, table, q_weight=None, k_weight=None, positions=None, eps:
     projection's output). Weights [D] of the same dtype (both None: rotation only); table from rope_table;
     positions int32 of the token shape, or None: 0..S-1 in each sequence (3-D: one sequence).
     Returns contiguous q and k, as attn_fwd takes them."""
-    T, S, Hq, Hkv, D, ld_q, ld_k = _qk_args(q, k, table, q_weight, k_weight, positions)
-    code = _dtype_code(q)
-    _on_current_device(q, k, table, q_weight, k_weight, positions)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-    _check(lib().sas_qk_norm_rope(code, _addr(q), ld_q, _addr(k), ld_k, _addr(q_weight), _addr(k_weight),
-                                  _addr(table), table.shape[0], _addr(positions), S, T, Hq, Hkv, D, eps,
-                                  _addr(q_out), _addr(k_out), _stream()))
+    code, args, (*_, dev) = _qk_args(q, k, table, q_weight, k_weight, positions, eps)
+    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
+    code = lib().sas_qk_norm_rope(code, *args, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(dev))
+    if code:
+        _check(code)
     return q_out, k_out
 
 
@@ -472,66 +494,53 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, q_weight=None, k_weight=None, 
                      workspace=None):
     """Gradients of qk_norm_rope: dq_out, dk_out (contiguous) are those of its outputs, the other arguments
     its inputs. Returns dq, dk (input dtype, contiguous) and the weights' gradients in fp32 (None without)."""
-    T, S, Hq, Hkv, D, ld_q, ld_k = _qk_args(q, k, table, q_weight, k_weight, positions)
-    code = _dtype_code(q)
-    _expect("dq_out", dq_out, q.dtype, q.shape)
-    _expect("dk_out", dk_out, q.dtype, k.shape)
-    _on_current_device(q, k, dq_out, dk_out, table, q_weight, k_weight, positions, workspace)
-    dev = q.device
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    code, args, (T, Hq, Hkv, D, dev) = _qk_args(q, k, table, q_weight, k_weight, positions, eps)
+    up = (_expect("dq_out", dq_out, q.dtype, q.shape, dev), _expect("dk_out", dk_out, q.dtype, k.shape, dev))
+    dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
     dwq = dwk = None
     if q_weight is not None:
-        dwq = torch.empty(D, dtype=torch.float32, device=dev)
-        dwk = torch.empty(D, dtype=torch.float32, device=dev)
-    if workspace is None:
-        need = int(lib().sas_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _check(lib().sas_qk_norm_rope_bwd(code, _addr(dq_out), _addr(dk_out), _addr(q), ld_q, _addr(k), ld_k,
-                                      _addr(q_weight), _addr(k_weight), _addr(table), table.shape[0],
-                                      _addr(positions), S, T, Hq, Hkv, D, eps, _addr(dq), _addr(dk), _addr(dwq),
-                                      _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(),
-                                      _stream()))
+        dwq, dwk = q.new_empty((2, D), dtype=_F32T).unbind()
+    L = lib()
+    ws, ws_bytes, workspace = _workspace(workspace, L.sas_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D), dev, q)
+    code = L.sas_qk_norm_rope_bwd(code, *up, *args, dq.data_ptr(), dk.data_ptr(), _addr(dwq), _addr(dwk), ws, ws_bytes,
+                                  _raw_stream(dev))
+    if code:
+        _check(code)
     return dq, dk, dwq, dwk
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _append(q8, q, k, v, table, k_cache, v_cache, scales, page_table, kv_len, q_weight, k_weight, cu_new, max_new, eps,
             kpool, with_k, page_size):
     T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    P = k_cache.shape[0]
-    N = kv_len.shape[0]
-    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.shape != (T, H, D):
-            raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
-    dt = torch.float8_e4m3fn if q8 else torch.bfloat16
-    _expect("table", table, torch.float32, (table.shape[0], D))
-    _expect("k_cache", k_cache, dt, (P, Hkv, page_size, D))
-    _expect("v_cache", v_cache, dt, (P, Hkv, page_size, D))
-    for name, t in zip(("k_scale", "v_scale"), scales):
-        _expect(name, t, torch.float32, (P, Hkv))
-    _expect("page_table", page_table, torch.int32, (N, page_table.shape[-1]))
-    _expect("kv_len", kv_len, torch.int32, (N,))
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight go together")
-    if q_weight is not None:
-        _expect("q_weight", q_weight, torch.bfloat16, (D,))
-        _expect("k_weight", k_weight, torch.bfloat16, (D,))
-    if cu_new is not None:
-        _expect("cu_new", cu_new, torch.int32, (N + 1,))
-    if kpool is not None:
-        _expect("kpool", kpool, torch.float32, (P, Hkv, D))
-    ld_q, ld_k, ld_v = _token_rows("q", q, T, Hq, D), _token_rows("k", k, T, Hkv, D), _token_rows("v", v, T, Hkv, D)
-    _on_current_device(q, k, v, table, k_cache, v_cache, *scales, page_table, kv_len, q_weight, k_weight, cu_new, kpool)
-    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device) if with_k else None
+    Hkv, P, N = k.shape[1], k_cache.shape[0], kv_len.shape[0]
+    max_pos, max_pages = table.shape[0], page_table.shape[-1]
+    dev = q.get_device()
+    dt = _F8 if q8 else _BF16
+    pages = (P, Hkv, page_size, D)
+    ld_q = _expect_rows("q", q, _BF16, (T, Hq, D), dev)
+    ld_k = _expect_rows("k", k, _BF16, (T, Hkv, D), dev)
+    ld_v = _expect_rows("v", v, _BF16, (T, Hkv, D), dev)
+    tab = _expect("table", table, _F32T, (max_pos, D), dev)
+    store = [_expect("k_cache", k_cache, dt, pages, dev), _expect("v_cache", v_cache, dt, pages, dev)]
+    if q8:
+        store += [_expect("k_scale", scales[0], _F32T, (P, Hkv), dev), _expect("v_scale", scales[1], _F32T, (P, Hkv), dev)]
+    pt = _expect("page_table", page_table, _I32, (N, max_pages), dev)
+    kv = _expect("kv_len", kv_len, _I32, (N,), dev)
+    w = _weight_ptrs(q_weight, k_weight, _BF16, D, dev)
+    cu = None if cu_new is None else _expect("cu_new", cu_new, _I32, (N + 1,), dev)
+    pool = None if kpool is None else _expect("kpool", kpool, _F32T, (P, Hkv, D), dev)
+    _expect_current(dev)
+    q_out = q.new_empty((T, Hq, D))
+    k_out = k.new_empty((T, Hkv, D)) if with_k else None
     fn = lib().sas_append_paged_q8 if q8 else lib().sas_append_paged
-    _check(fn(_addr(q), ld_q, _addr(k), ld_k, _addr(v), ld_v, _addr(q_weight), _addr(k_weight), _addr(table),
-              table.shape[0], _addr(cu_new), N, max_new, T, _addr(kv_len), _addr(page_table), page_table.shape[1], P,
-              Hq, Hkv, D, page_size, eps, _addr(q_out), _addr(k_out), _addr(k_cache), _addr(v_cache),
-              *map(_addr, scales), _addr(kpool), _stream()))
+    code = fn(q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, *w, tab, max_pos, cu, N, max_new, T, kv, pt,
+              max_pages, P, Hq, Hkv, D, page_size, eps, q_out.data_ptr(), _addr(k_out), *store, pool, _raw_stream(dev))
+    if code:
+        _check(code)
     return (q_out, k_out) if with_k else q_out
 
 
