@@ -402,7 +402,7 @@ sas_status sas_decode_paged_q8(const void *q, const void *k_cache, const void *v
  *            outside 0 .. max_pos-1 is flagged and its output rows are zero.
  * q_out, k_out  device [T, Hq, D], [T, Hkv, D], contiguous, 16-byte aligned (output);
  *            they must not overlap the inputs.
- * D in {64, 128}; T x heads up to 2^31 - 1. eps > 0.
+ * D in {64, 128}; T * (Hq + Hkv) up to 2^31 - 1. eps > 0.
  */
 sas_status sas_qk_norm_rope(sas_dtype dtype, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
                             const void *q_weight, const void *k_weight, const float *rope_table,

@@ -68,7 +68,7 @@ def _adds(T, H, D):
     return 4 + max(1, math.ceil(units / slots)) + slots + 64
 
 
-def _compare(dtype, D, shape, Hq, Hkv, table, x, weights=True, positions=True):
+def _compare(dtype, D, shape, Hq, Hkv, table, x, weights=True, positions=True, adds=None):
     q, k, w, dq, dk, pos = x
     h = DTYPES[dtype][1]
     T = math.prod(shape)
@@ -92,7 +92,7 @@ def _compare(dtype, D, shape, Hq, Hkv, table, x, weights=True, positions=True):
         dx, dw, mag, wmag = R.norm_rope_bwd(up.reshape(T, H, D), rows, wt, tab, at, EPS)
         _check(grads[i].reshape(T, H, D), dx, h * np.abs(dx) + 80 * U * mag, "d" + name)
         if weights:
-            _check(grads[2 + i], dw, (17 + _adds(T, H, D)) * U * wmag, f"d{name}_weight")
+            _check(grads[2 + i], dw, (17 + (adds or _adds(T, H, D))) * U * wmag, f"d{name}_weight")
         else:
             assert grads[2 + i] is None
     return y, grads
@@ -117,11 +117,15 @@ def test_without_positions_or_weights(dtype, D, shape, fused, weights, positions
     _compare(dtype, D, shape, 4, 2, table, x, weights=weights, positions=positions)
 
 
-def test_many_tokens_use_every_cta():
-    """More units than the gradient kernel's CTAs hold at a time."""
-    table = sas.rope_table(70000, 64)
-    x = _make("bf16", 64, (9001,), 12, 4, seed=5)
-    _compare("bf16", 64, (9001,), 12, 4, table, x)
+@pytest.mark.parametrize("dtype,D,T,Hq,Hkv", [("bf16", 64, 9001, 12, 4), ("bf16", 128, 4001, 40, 8),
+                                              ("f32", 128, 1601, 40, 8)])
+def test_many_tokens_use_every_cta(dtype, D, T, Hq, Hkv):
+    """More units than the resident CTAs hold at a time; the last two are beyond eight for each row slot, where
+    a CTA does query and key units. Additions of a weight gradient's sum: at most 4 in a unit, 20 units of a
+    slot, 64 slots, 32 in each of the last two steps."""
+    table = sas.rope_table(70000, D)
+    x = _make(dtype, D, (T,), Hq, Hkv, seed=5)
+    _compare(dtype, D, (T,), Hq, Hkv, table, x, adds=4 + 20 + 64 + 64)
 
 
 def test_extreme_rows():

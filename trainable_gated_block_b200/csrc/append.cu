@@ -46,12 +46,28 @@ __device__ __forceinline__ int seq_of_row(const AppendArgs& a, long long t) {
     return __ldg(a.cu_new + lo) <= t && t < __ldg(a.cu_new + lo + 1) ? lo : -1;
 }
 
+constexpr int kHeads = 4;       // query heads of one token that a row slot takes
+
 template <int D>
-__device__ __forceinline__ void append_q(const AppendArgs& a, long long cta) {
+__device__ __forceinline__ void append_q(const AppendArgs& a, uint32_t cta) {
     constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
-    const int l = threadIdx.x % HeadRow<D>::kLanes, parts = unit_parts(a.Hq);
-    const long long u = cta * kSlots + threadIdx.x / HeadRow<D>::kLanes;
-    const long long t = u / parts;
+    const int l = threadIdx.x % HeadRow<D>::kLanes;
+    const uint32_t parts = ((uint32_t)a.Hq + kHeads - 1) / kHeads;
+    const uint32_t u = cta * kSlots + threadIdx.x / HeadRow<D>::kLanes, t = u / parts, h0 = u - t * parts;
+    // the rows' loads are on their way before the token's sequence is looked for
+    const bf16* src = static_cast<const bf16*>(a.q) + (t < a.T ? t * a.ld_q : 0) + 8 * l;
+    uint4 lo[kHeads][1], hi[kHeads][1];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int h = (int)(h0 + i * parts);
+        lo[i][0] = hi[i][0] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < a.T && h < a.Hq) {
+            lo[i][0] = ld_stream(src + h * D);
+            hi[i][0] = ld_stream(src + h * D + D / 2);
+        }
+    }
+    const bf16* weight = static_cast<const bf16*>(a.q_weight);
+    const Row w = load_weight<bf16, D>(weight, l);
     // -1: a padding entry, whose row is zero; rows of no sequence, or of one that is skipped, stay as they are
     int pos = -1;
     bool live = t < a.T;
@@ -64,37 +80,62 @@ __device__ __forceinline__ void append_q(const AppendArgs& a, long long cta) {
             if (s.count > 0) pos = s.first + (int)(t - s.row0);
         }
     }
-    norm_rope_unit<bf16, D>(static_cast<const bf16*>(a.q) + (live ? t * a.ld_q : 0),
-                            static_cast<bf16*>(a.q_out) + t * a.Hq * D, a.Hq, (int)(u % parts),
-                            static_cast<const bf16*>(a.q_weight), a.table, a.eps, l, live, [&] { return pos; });
+    const Turn turn(load_angles<bf16, D>(a.table, live ? max(pos, 0) : 0, l), w);
+    bf16* dst = static_cast<bf16*>(a.q_out) + (long long)t * a.Hq * D;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int h = (int)(h0 + i * parts);
+        Row x;
+        x.a = Raw8<bf16>::get(lo[i]);
+        x.b = Raw8<bf16>::get(hi[i]);
+        Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+        if (pos < 0) y.a = y.b = Half{};
+        if (live && h < a.Hq) {
+            store_row<D>(dst + h * D, l, y);
+        }
+    }
 }
 
-// Eight e4m3 codes (8 bytes) from eight values, and back.
-__device__ __forceinline__ uint2 to_codes(const float* x, float inv) {
-    uint32_t w[2];
+// Eight e4m3 codes (8 bytes) from eight values times inv, and back.
+__device__ __forceinline__ uint2 to_codes(const Half& x, float inv) {
+    const f2 ii = f2_pack(inv, inv);
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | hi << 16;
-    }
-    return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(f2_unpack(f2_mul(x.v[i], ii)), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
-__device__ __forceinline__ void from_codes(uint2 c, float* x) {
+__device__ __forceinline__ Half from_codes(uint2 c) {
     const uint32_t w[2] = {c.x, c.y};
+    Half h;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+        h.v[i] = f2_pack(f.x, f.y);
     }
+    return h;
+}
+__device__ __forceinline__ void add(Half& s, const Half& x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.v[i] = f2_add(s.v[i], x.v[i]);
+}
+// An infinity has no code: it is kept as NaN. Returns the largest finite magnitude so far.
+__device__ __forceinline__ float finite_max(Half& x, float m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f = f2_unpack(x.v[i]);
+        if (!(fabsf(f.x) <= 3.402823466e38f)) f.x = __int_as_float(0x7fffffff);
+        if (!(fabsf(f.y) <= 3.402823466e38f)) f.y = __int_as_float(0x7fffffff);
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+        x.v[i] = f2_pack(f.x, f.y);
+    }
+    return m;
 }
 
 template <int D, bool kQ8>
 __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
     constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
-    __shared__ float red[kSlots][D];
+    __shared__ __align__(16) float red[kSlots][D];
     __shared__ float wmax[kThreads / 32];
     const int tiles = max_tiles(a.max_new);
     const int h = (int)(item % a.Hkv);
@@ -109,9 +150,7 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
     }
     bf16* k_out = static_cast<bf16*>(a.k_out);
     if (s.count == 0 && a.cu_new == nullptr && k_out != nullptr && !is_v && slot == 0) {   // a padding entry
-        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        store8(k_out + ((long long)n * a.Hkv + h) * D + 8 * l, zero);
-        store8(k_out + ((long long)n * a.Hkv + h) * D + D / 2 + 8 * l, zero);
+        store_row<D>(k_out + ((long long)n * a.Hkv + h) * D, l, Row{});
     }
     const PageTile t = page_tile(s, (int)(nt % tiles));
     if (t.hi <= t.lo) return;
@@ -123,71 +162,51 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
     }
 
     // the new rows, one for each of kRows steps of a slot
-    const bf16* src = is_v ? static_cast<const bf16*>(a.v) + h * D : static_cast<const bf16*>(a.k) + h * D;
+    const bf16* src = (is_v ? static_cast<const bf16*>(a.v) : static_cast<const bf16*>(a.k)) + h * D + 8 * l;
     const long long ld = is_v ? a.ld_v : a.ld_k;
-    Raw8<bf16> lo[kRows], hi[kRows];
+    uint4 lo[kRows][1], hi[kRows][1];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int r = slot + i * kSlots;
-        lo[i].zero();
-        hi[i].zero();
+        lo[i][0] = hi[i][0] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= t.lo && r < t.hi) {
-            const bf16* p = src + (t.row + r - t.lo) * ld + 8 * l;
-            lo[i].load(p);
-            hi[i].load(p + D / 2);
+            const bf16* p = src + (t.row + r - t.lo) * ld;
+            lo[i][0] = ld_stream(p);
+            hi[i][0] = ld_stream(p + D / 2);
         }
     }
-    float x[kRows][16];
     const bf16* weight = static_cast<const bf16*>(a.k_weight);
-    float w[16];
-    if (!is_v && weight != nullptr) load_weight<bf16, D>(weight, l, w);
+    Row w;
+    if (!is_v) w = load_weight<bf16, D>(weight, l);
+    Row x[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        lo[i].get(x[i]);
-        hi[i].get(x[i] + 8);
+        x[i].a = Raw8<bf16>::get(lo[i]);
+        x[i].b = Raw8<bf16>::get(hi[i]);
         if (is_v) continue;
         const int r = slot + i * kSlots;
-        if (weight != nullptr) {
-            const float rr = row_rrms<D>(x[i], a.eps);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[i][e] = x[i][e] * rr * w[e];
-        }
+        const float rr = weight != nullptr ? row_rrms<D>(x[i], a.eps) : 1.f;
         if (r >= t.lo && r < t.hi) {
-            Angles ang;
-            ang.load<D>(a.table, t.block * kPageRows + r, l);
-            ang.turn(x[i]);
-            if (k_out != nullptr) {
-                bf16* p = k_out + ((t.row + r - t.lo) * a.Hkv + h) * D + 8 * l;
-                store8(p, x[i]);
-                store8(p + D / 2, x[i] + 8);
-            }
+            x[i] = Turn(load_angles<bf16, D>(a.table, t.block * kPageRows + r, l), w)(x[i], rr);
+            if (k_out != nullptr) store_row<D>(k_out + ((t.row + r - t.lo) * a.Hkv + h) * D, l, x[i]);
         }
     }
     if (!page_ok) return;
     const long long tile0 = ((long long)page * a.Hkv + h) * kPageRows;      // row of the cache
     const bool pool = a.kpool != nullptr && !is_v && t.hi == kPageRows;
-    float sum[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+    Row sum{};
     float unit = 1.f;               // what a pooled value is in
 
     if constexpr (kQ8) {
-        uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D;
+        uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D + 8 * l;
         float* scale = (is_v ? a.v_scale : a.k_scale) + (long long)page * a.Hkv + h;
-        float m = 0.f;
+        const float old = t.lo > 0 ? *scale : 0.f;
+        float m = 0.f;              // rows that are not new are zero here
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                // an infinity has no code: it is kept as NaN, and no scale follows it
-                if (!(fabsf(x[i][e]) <= 3.402823466e38f)) x[i][e] = __int_as_float(0x7fffffff);
-                const int r = slot + i * kSlots;
-                if (r >= t.lo && r < t.hi) m = fmaxf(m, fabsf(x[i][e]));
-            }
+        for (int i = 0; i < kRows; ++i) m = finite_max(x[i].b, finite_max(x[i].a, m));
         m = warp_max(m);
         if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-        const float old = t.lo > 0 ? *scale : 0.f;
-        __syncthreads();
+        __syncthreads();            // (and every thread has read the old scale)
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
         if (t.lo > 0 && !scale_ok(old)) {       // the rows already there have no value
@@ -202,35 +221,24 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = slot + i * kSlots;
-            if (r >= t.hi) continue;
-            uint2* p = reinterpret_cast<uint2*>(cache + r * D + 8 * l);
-            uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2 + 8 * l);
+            if (r >= t.hi || (r < t.lo && keep && !pool)) continue;
+            uint2* p = reinterpret_cast<uint2*>(cache + r * D);
+            uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2);
             uint2 c, c2;
             if (r >= t.lo) {
-                c = to_codes(x[i], inv);
-                c2 = to_codes(x[i] + 8, inv);
-                *p = c;
-                *p2 = c2;
+                *p = c = to_codes(x[i].a, inv);
+                *p2 = c2 = to_codes(x[i].b, inv);
             } else {
-                if (keep && !pool) continue;
                 c = *p;
                 c2 = *p2;
                 if (!keep) {
-                    float y[16];
-                    from_codes(c, y);
-                    from_codes(c2, y + 8);
-                    c = to_codes(y, ratio);
-                    c2 = to_codes(y + 8, ratio);
-                    *p = c;
-                    *p2 = c2;
+                    *p = c = to_codes(from_codes(c), ratio);
+                    *p2 = c2 = to_codes(from_codes(c2), ratio);
                 }
             }
             if (pool) {
-                float y[16];
-                from_codes(c, y);
-                from_codes(c2, y + 8);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) sum[e] += y[e];
+                add(sum.a, from_codes(c));
+                add(sum.b, from_codes(c2));
             }
         }
     } else {
@@ -238,35 +246,21 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = slot + i * kSlots;
-            bf16* p = cache + r * D + 8 * l;
-            if (r >= t.lo && r < t.hi) {
-                store8(p, x[i]);
-                store8(p + D / 2, x[i] + 8);
-            }
-            if (pool) {
-                float y[16];
-                if (r < t.lo) {
-                    Raw8<bf16> u, v;
-                    u.w = *reinterpret_cast<const uint4*>(p);
-                    v.w = *reinterpret_cast<const uint4*>(p + D / 2);
-                    u.get(y);
-                    v.get(y + 8);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = __bfloat162float(__float2bfloat16_rn(x[i][e]));
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) sum[e] += y[e];
+            if (r >= t.lo && r < t.hi) store_row<D>(cache + r * D, l, x[i]);
+            if (pool) {             // what this thread has stored, or an older row
+                const bf16* p = cache + r * D + 8 * l;
+                const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)}, v[1] = {*reinterpret_cast<const uint4*>(p + D / 2)};
+                add(sum.a, Raw8<bf16>::get(u));
+                add(sum.b, Raw8<bf16>::get(v));
             }
         }
     }
     if (!pool) return;
     // the filled page's mean key: the slots' sums in slot order
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        red[slot][8 * l + e] = sum[e];
-        red[slot][D / 2 + 8 * l + e] = sum[e + 8];
-    }
+    *reinterpret_cast<ulonglong2*>(&red[slot][8 * l]) = make_ulonglong2(sum.a.v[0], sum.a.v[1]);
+    *reinterpret_cast<ulonglong2*>(&red[slot][8 * l + 4]) = make_ulonglong2(sum.a.v[2], sum.a.v[3]);
+    *reinterpret_cast<ulonglong2*>(&red[slot][D / 2 + 8 * l]) = make_ulonglong2(sum.b.v[0], sum.b.v[1]);
+    *reinterpret_cast<ulonglong2*>(&red[slot][D / 2 + 8 * l + 4]) = make_ulonglong2(sum.b.v[2], sum.b.v[3]);
     __syncthreads();
     if (threadIdx.x < D) {
         float m = 0.f;
@@ -286,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, lo
 template <int D, bool kQ8>
 cudaError_t go(const AppendArgs& a, cudaStream_t st) {
     constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
-    const long long q_ctas = a.q != nullptr ? (a.T * unit_parts(a.Hq) + kSlots - 1) / kSlots : 0;
+    const long long q_ctas = a.q != nullptr ? (a.T * ((a.Hq + kHeads - 1) / kHeads) + kSlots - 1) / kSlots : 0;
     append_kernel<D, kQ8><<<(unsigned)(q_ctas + append_kv_ctas(a)), kThreads, 0, st>>>(a, q_ctas);
     count_launches(1);
     return cudaGetLastError();

@@ -1,15 +1,29 @@
 // One head row (D values) held by D / 16 neighbouring lanes, for the kernels
 // that norm and rotate queries and keys.
 //
-// Lane l of a row holds the dimensions 8l .. 8l+7 and D/2 + 8l .. D/2 + 8l+7:
-// both halves of its eight rotation pairs (i, i + D/2), so the rotation needs
-// no exchange between lanes, and each half is one 16-byte access in bf16 (two
-// in fp32). Only the sum of squares crosses the row's lanes.
+// Lane l of a row holds eight dimensions of its lower half and the same eight
+// of its upper half: both values of its rotation pairs (i, i + D/2), so the
+// rotation needs no exchange between lanes. Each half is one 16-byte access in
+// bf16 (8l .. 8l+7) and two in fp32 (4l .. 4l+3 and D/4 + 4l .. + 3), so that the
+// lanes of a row always touch neighbouring 16-byte pieces: with 32 consecutive
+// bytes for each lane in fp32 every sector moved twice (65% of the copy rate
+// instead of HBM's). Only the sum of squares crosses the row's lanes. Values are kept
+// two to a 64-bit register for the f32x2 arithmetic of sm_100a (each half is
+// rounded like the scalar instruction), which halves the instructions of rows
+// that are otherwise bound by HBM.
 #pragma once
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace sas {
+
+using f2 = unsigned long long;
+using sm100::f2_add;
+using sm100::f2_fma;
+using sm100::f2_mul;
+using sm100::f2_pack;
+using sm100::f2_unpack;
 
 template <int D>
 struct HeadRow {
@@ -18,8 +32,42 @@ struct HeadRow {
     static constexpr int kPerWarp = 32 / kLanes;     // rows a warp holds at a time
 };
 
-// Eight consecutive values at p (16-byte aligned), as fp32. Inputs are read
-// once: they bypass L1, which the rotation table's rows are to stay in.
+// A lane's 16 values: a of the lower half of the row, b those D/2 further.
+struct Half {
+    f2 v[4];
+};
+struct Row {
+    Half a, b;
+};
+
+// Eight consecutive values as loaded: 16-byte pieces.
+// Piece i of lane l starts at dimension i * D / 4 + l * kStep of the half row.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    static constexpr int kPieces = 1, kStep = 8;
+    static __device__ __forceinline__ Half get(const uint4 (&p)[1]) {
+        const uint32_t w[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+        Half h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2_to_f32(w[i]);
+            h.v[i] = f2_pack(f.x, f.y);
+        }
+        return h;
+    }
+};
+template <> struct Raw8<float> {
+    static constexpr int kPieces = 2, kStep = 4;
+    static __device__ __forceinline__ Half get(const uint4 (&p)[2]) {
+        const uint32_t w[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
+        Half h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h.v[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        return h;
+    }
+};
+
+// Inputs are read once: they bypass L1, which the rotation table's rows are to stay in.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 w;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -27,51 +75,27 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                  : "l"(p));
     return w;
 }
-template <typename T> struct Raw8;                   // eight values as loaded
-template <> struct Raw8<__nv_bfloat16> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = ld_stream(p); }
-    __device__ __forceinline__ void load_cached(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float* x) const {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = bf16x2_to_f32(v[e]);
-            x[2 * e] = f.x;
-            x[2 * e + 1] = f.y;
-        }
-    }
-};
-template <> struct Raw8<float> {
-    uint4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = ld_stream(p);
-        b = ld_stream(p + 4);
-    }
-    __device__ __forceinline__ void load_cached(const float* p) {
-        a = __ldg(reinterpret_cast<const uint4*>(p));
-        b = __ldg(reinterpret_cast<const uint4*>(p + 4));
-    }
-    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float* x) const {
-        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[e]);
-    }
-};
 
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t bf16x2_of(f2 v) {
+    const float2 f = f2_unpack(v);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]), bf16x2_of(x[4], x[5]), bf16x2_of(x[6], x[7]));
+// The lane's eight values to a half row at p.
+template <int D>
+__device__ __forceinline__ void store_half(__nv_bfloat16* p, int l, const Half& h) {
+    *reinterpret_cast<uint4*>(p + 8 * l) =
+        make_uint4(bf16x2_of(h.v[0]), bf16x2_of(h.v[1]), bf16x2_of(h.v[2]), bf16x2_of(h.v[3]));
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+template <int D>
+__device__ __forceinline__ void store_half(float* p, int l, const Half& h) {
+    *reinterpret_cast<ulonglong2*>(p + 4 * l) = make_ulonglong2(h.v[0], h.v[1]);
+    *reinterpret_cast<ulonglong2*>(p + D / 4 + 4 * l) = make_ulonglong2(h.v[2], h.v[3]);
+}
+template <int D, typename T>
+__device__ __forceinline__ void store_row(T* p, int l, const Row& r) {
+    store_half<D>(p, l, r.a);
+    store_half<D>(p + D / 2, l, r.b);
 }
 
 // Sum over the lanes of a row (all lanes of the warp take part).
@@ -81,110 +105,112 @@ __device__ __forceinline__ float row_sum(float x) {
     for (int o = HeadRow<D>::kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+__device__ __forceinline__ float f2_sum(f2 v) {
+    const float2 f = f2_unpack(v);
+    return f.x + f.y;
+}
+
+// Sum over the row of the products of two rows' values.
+template <int D>
+__device__ __forceinline__ float row_dot(const Row& x, const Row& y) {
+    f2 s = f2_mul(x.a.v[0], y.a.v[0]), t = f2_mul(x.b.v[0], y.b.v[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        s = f2_fma(x.a.v[i], y.a.v[i], s);
+        t = f2_fma(x.b.v[i], y.b.v[i], t);
+    }
+    return row_sum<D>(f2_sum(f2_add(s, t)));
+}
 
 // 1 / rms of the row: rsqrt(mean(x^2) + eps), in fp32.
 template <int D>
-__device__ __forceinline__ float row_rrms(const float (&x)[16], float eps) {
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-    return rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+__device__ __forceinline__ float row_rrms(const Row& x, float eps) {
+    return rsqrtf(row_dot<D>(x, x) * (1.f / D) + eps);
 }
 
 // The lane's eight angles of one position: cos and sin from a table row
 // [cos(D/2) | sin(D/2)] in fp32.
 struct Angles {
-    float c[8], s[8];
-    template <int D>
-    __device__ __forceinline__ void load(const float* table, int pos, int l) {
-        const float* row = table + (long long)pos * D + 8 * l;
+    Half c, s;
+};
+template <typename T, int D>
+__device__ __forceinline__ Angles load_angles(const float* table, int pos, int l) {
+    // in 16-byte pieces: the second four dimensions of the lane's eight follow the first, or lie D / 4 further
+    constexpr int kSecond = sizeof(T) == 2 ? 1 : D / 16;
+    const ulonglong2* row = reinterpret_cast<const ulonglong2*>(table + (long long)pos * D + Raw8<T>::kStep * l);
+    const ulonglong2 c0 = __ldg(row), c1 = __ldg(row + kSecond), s0 = __ldg(row + D / 8), s1 = __ldg(row + D / 8 + kSecond);
+    Angles g;
+    g.c.v[0] = c0.x, g.c.v[1] = c0.y, g.c.v[2] = c1.x, g.c.v[3] = c1.y;
+    g.s.v[0] = s0.x, g.s.v[1] = s0.y, g.s.v[2] = s1.x, g.s.v[3] = s1.y;
+    return g;
+}
+
+// The lane's 16 weights of a head norm (ones without weights).
+template <typename T, int D>
+__device__ __forceinline__ Row load_weight(const T* w, int l) {
+    Row r;
+    if (w == nullptr) {
+        const f2 one = f2_pack(1.f, 1.f);
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(row + e));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(row + D / 2 + e));
-            c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
-            s[e] = b.x, s[e + 1] = b.y, s[e + 2] = b.z, s[e + 3] = b.w;
+        for (int i = 0; i < 4; ++i) r.a.v[i] = r.b.v[i] = one;
+        return r;
+    }
+    uint4 p[Raw8<T>::kPieces], q[Raw8<T>::kPieces];
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::kPieces; ++i) {
+        const T* at = w + i * (D / 4) + Raw8<T>::kStep * l;
+        p[i] = __ldg(reinterpret_cast<const uint4*>(at));
+        q[i] = __ldg(reinterpret_cast<const uint4*>(at + D / 2));
+    }
+    r.a = Raw8<T>::get(p);
+    r.b = Raw8<T>::get(q);
+    return r;
+}
+
+// Weight and rotation in one: y_a = r (x_a (w_a c) - x_b (w_b s)), y_b = r (x_b (w_b c) + x_a (w_a s)),
+// with coefficients that all heads of a token share.
+struct Turn {
+    Half ac, bs, bc, as;        // w_a c, -(w_b s), w_b c, w_a s
+    __device__ __forceinline__ Turn(const Angles& g, const Row& w) {
+        const f2 neg = f2_pack(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ac.v[i] = f2_mul(w.a.v[i], g.c.v[i]);
+            bs.v[i] = f2_mul(f2_mul(w.b.v[i], g.s.v[i]), neg);
+            bc.v[i] = f2_mul(w.b.v[i], g.c.v[i]);
+            as.v[i] = f2_mul(w.a.v[i], g.s.v[i]);
         }
     }
-    // (x_i, x_{i + D/2}) turned by the angle; `back` by its negative (the transpose).
-    __device__ __forceinline__ void turn(float (&x)[16]) const {
+    __device__ __forceinline__ Row operator()(const Row& x, float r) const {
+        const f2 rr = f2_pack(r, r);
+        Row y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = x[e], b = x[e + 8];
-            x[e] = fmaf(a, c[e], -b * s[e]);
-            x[e + 8] = fmaf(b, c[e], a * s[e]);
+        for (int i = 0; i < 4; ++i) {
+            y.a.v[i] = f2_mul(rr, f2_fma(x.a.v[i], ac.v[i], f2_mul(x.b.v[i], bs.v[i])));
+            y.b.v[i] = f2_mul(rr, f2_fma(x.b.v[i], bc.v[i], f2_mul(x.a.v[i], as.v[i])));
         }
-    }
-    __device__ __forceinline__ void turn_back(float (&x)[16]) const {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = x[e], b = x[e + 8];
-            x[e] = fmaf(a, c[e], b * s[e]);
-            x[e + 8] = fmaf(b, c[e], -a * s[e]);
-        }
+        return y;
     }
 };
 
-// The lane's 16 weights of a head norm.
-template <typename T, int D>
-__device__ __forceinline__ void load_weight(const T* w, int l, float (&x)[16]) {
-    Raw8<T> a, b;
-    a.load_cached(w + 8 * l);
-    b.load_cached(w + D / 2 + 8 * l);
-    a.get(x);
-    b.get(x + 8);
+// 16 bytes from global to shared memory without a register (zeroes without
+// `live`); each thread copies and later reads its own pieces only, so that the
+// groups need no barrier.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-
-constexpr int kUnitHeads = 4;       // heads of one token that a row slot takes
-
-__host__ __device__ __forceinline__ int unit_parts(int H) { return (H + kUnitHeads - 1) / kUnitHeads; }
-
-// Norm and rotation of the heads h0, h0 + parts, ... of one token row (`src`
-// to `dst`, both [H, D]) by the lanes of a row slot. The rows' loads are
-// issued before `position()` is asked for, which may have to search. A
-// negative position writes zeros; without `live` nothing is read or written
-// (the lanes still take part in the warp's sums).
-template <typename T, int D, typename Position>
-__device__ __forceinline__ void norm_rope_unit(const T* src, T* dst, int H, int h0, const T* weight, const float* table,
-                                               float eps, int l, bool live, Position position) {
-    const int parts = unit_parts(H);
-    Raw8<T> lo[kUnitHeads], hi[kUnitHeads];
-#pragma unroll
-    for (int i = 0; i < kUnitHeads; ++i) {
-        const int h = h0 + i * parts;
-        lo[i].zero();
-        hi[i].zero();
-        if (live && h < H) {
-            lo[i].load(src + h * D + 8 * l);
-            hi[i].load(src + h * D + D / 2 + 8 * l);
-        }
-    }
-    const int pos = live ? position() : -1;
-    Angles ang;
-    ang.load<D>(table, max(pos, 0), l);
-    float w[16];
-    if (weight != nullptr) load_weight<T, D>(weight, l, w);
-#pragma unroll
-    for (int i = 0; i < kUnitHeads; ++i) {
-        const int h = h0 + i * parts;
-        float x[16];
-        lo[i].get(x);
-        hi[i].get(x + 8);
-        if (weight != nullptr) {
-            const float r = row_rrms<D>(x, eps);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
-        }
-        ang.turn(x);
-        if (pos < 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
-        }
-        if (live && h < H) {
-            store8(dst + h * D + 8 * l, x);
-            store8(dst + h * D + D / 2 + 8 * l, x + 8);
-        }
-    }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t p) {
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(p)
+                 : "memory");
+    return w;
 }
 
 }  // namespace sas

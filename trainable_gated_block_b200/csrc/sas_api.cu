@@ -179,7 +179,7 @@ sas_status check_norm_rope(const char* fn, sas_dtype dtype, const void* q, int64
     if (T < 0) return fail(SAS_ERR_INVALID_ARG, "%s: T=%lld", fn, (long long)T);
     if (T == 0) return SAS_OK;
     if (!positions && S <= 0) return fail(SAS_ERR_INVALID_ARG, "%s: S=%d without positions", fn, S);
-    if (T > ((1LL << 31) - 1) / (Hq > Hkv ? Hq : Hkv)) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^31", fn);
+    if (T > ((1LL << 31) - 1) / (Hq + Hkv)) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^31", fn);
     const int elem = dtype == SAS_BF16 ? 2 : 4;
     if ((r = check_rows(fn, "q", q, ld_q, Hq, D, elem)) != SAS_OK) return r;
     return check_rows(fn, "k", k, ld_k, Hkv, D, elem);
