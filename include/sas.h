@@ -440,9 +440,10 @@ sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void 
  * q, k, v    device bf16 [T, Hq, D], [T, Hkv, D], [T, Hkv, D], token strides ld_q, ld_k,
  *            ld_v as in sas_qk_norm_rope. q and q_out may both be NULL.
  * q_weight, k_weight, rope_table, max_pos, eps   as in sas_qk_norm_rope (bf16 weights).
- * cu_new     device int32 [N + 1]: sequence n brings the token rows cu_new[n] ..
- *            cu_new[n+1]-1, at most max_new of them (it may bring none). NULL: one token for
- *            each sequence (T = N, max_new = 1).
+ * cu_new     device int32 [N + 1], not decreasing: sequence n brings the token rows
+ *            cu_new[n] .. cu_new[n+1]-1, at most max_new of them (it may bring none).
+ *            Where it decreases the call is flagged, and other sequences may be left out
+ *            too. NULL: one token for each sequence (T = N, max_new = 1).
  * kv_len     device int32 [N]: tokens of each sequence with the new ones, which take the
  *            positions kv_len[n] - count .. kv_len[n] - 1 (so sas_decode_paged takes the
  *            same kv_len). At most 64 * max_pages and at most max_pos. Without cu_new,
@@ -458,7 +459,8 @@ sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void 
  * A sequence whose lengths break these terms is flagged and skipped whole; a page id
  * outside 0 .. num_pages-1 is flagged and the rows for that page are skipped. Rows of
  * q_out and k_out that belong to no sequence, or to a skipped one, are left as they are.
- * Outputs must not overlap the inputs. D in {64, 128}, page_size 64.
+ * Outputs must not overlap the inputs. D in {64, 128}, page_size 64, T * Hq and
+ * (T / 64 + 2 N) * Hkv below 2^29.
  */
 sas_status sas_append_paged(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
                             int64_t ld_v, const void *q_weight, const void *k_weight,

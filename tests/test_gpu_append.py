@@ -179,6 +179,36 @@ def test_pieces_of_prompts(q8, D, Hq, Hkv, starts, news):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 6, 3)])
+def test_single_tokens_of_some_sequences(q8, D, Hq, Hkv):
+    """cu_new with max_new 1: sequences that bring a token and others that bring none."""
+    starts, news = [63, 5, 130, 64, 0], [1, 0, 1, 0, 1]
+    P, pt = _layout(starts, news, seed=21)
+    kv = torch.tensor([s + n for s, n in zip(starts, news)], dtype=torch.int32)
+    cu = torch.tensor([0] + news).cumsum(0).to(torch.int32)
+    tok, dev = _tokens(3, Hq, Hkv, D, seed=22)
+    _check_call(Cache(q8, P, Hkv, D, seed=23), tok, dev, sas.rope_table(140, D), pt, kv, cu, 1)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_many_sequences_and_long_pieces(q8):
+    """More units and tiles than the resident CTAs take at a time, by token and by piece."""
+    D, Hq, Hkv = 128, 20, 4
+    g = torch.Generator().manual_seed(24)
+    starts = torch.randint(0, 300, (150,), generator=g).tolist()
+    P, pt = _layout(starts, [1] * 150, seed=25)
+    tok, dev = _tokens(150, Hq, Hkv, D, seed=26)
+    kv = torch.tensor([s + 1 for s in starts], dtype=torch.int32)
+    _check_call(Cache(q8, P, Hkv, D, seed=27), tok, dev, sas.rope_table(400, D), pt, kv, None, 1)
+    starts, news = [70, 0, 129], [2700, 1999, 641]
+    P, pt = _layout(starts, news, seed=28)
+    tok, dev = _tokens(sum(news), Hq, Hkv, D, seed=29)
+    kv = torch.tensor([s + n for s, n in zip(starts, news)], dtype=torch.int32)
+    cu = torch.tensor([0] + news).cumsum(0).to(torch.int32)
+    _check_call(Cache(q8, P, Hkv, D, seed=30), tok, dev, sas.rope_table(2800, D), pt, kv, cu, max(news))
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_rows_behind_the_last_sequence_stay(q8):
     """cu_new ends before T, and starts after row 0: the rows outside are neither stored nor written."""
     P, pt = _layout([5], [70], seed=4)

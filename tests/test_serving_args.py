@@ -71,7 +71,8 @@ AP = [FAKE, 512, FAKE, 256, FAKE, 256, FAKE, FAKE, FAKE, 64, None, 3, 1, 3, FAKE
     ({17: 0}, sas.SAS_ERR_INVALID_ARG), ({20: 96}, sas.SAS_ERR_UNSUPPORTED), ({21: 32}, sas.SAS_ERR_UNSUPPORTED),
     ({22: -1.0}, sas.SAS_ERR_INVALID_ARG), ({23: None}, sas.SAS_ERR_INVALID_ARG), ({24: ODD}, sas.SAS_ERR_INVALID_ARG),
     ({25: None}, sas.SAS_ERR_INVALID_ARG), ({27: ODD}, sas.SAS_ERR_INVALID_ARG),
-    ({10: FAKE, 13: 1 << 30}, sas.SAS_ERR_UNSUPPORTED), ({10: FAKE, 12: 1 << 30, 11: 64}, sas.SAS_ERR_UNSUPPORTED),
+    ({10: FAKE, 13: 1 << 30}, sas.SAS_ERR_UNSUPPORTED), ({10: FAKE, 12: (1 << 30) + 1}, sas.SAS_ERR_UNSUPPORTED),
+    ({10: FAKE, 11: 1 << 28}, sas.SAS_ERR_UNSUPPORTED),
     ({11: 0, 13: 0}, sas.SAS_OK), ({10: FAKE, 13: 0}, sas.SAS_OK)])
 def test_append_refusals(L, changes, code):
     assert L.sas_append_paged(*_with(AP, changes)) == code
@@ -200,6 +201,8 @@ extern "C" int tiles(int has_cu, int lo, int hi, int n, long long T, int max_new
     }
     return m;
 }
+extern "C" unsigned base(int lo, int n) { return sas::seq_tile_base(lo, n); }
+extern "C" int max_tiles(int n) { return sas::max_tiles(n); }
 extern "C" int sexp(unsigned bits) { return sas::scale_exp(bits); }
 extern "C" int ok(float s) { return sas::scale_ok(s); }
 ''')
@@ -227,6 +230,18 @@ def test_tiles_cover_each_new_row_once(rows, start, count, slack):
     want = [(p // 64, p % 64, 10 + p - start) for p in range(start, start + count)]
     assert [(b, r, row + r - lo) for b, lo, hi, row in got for r in range(lo, hi)] == want
     assert len({b for b, *_ in got}) == len(got)
+
+
+def test_tile_indices_suffice_for_every_sequence(rows):
+    """Between the tile bases of neighbouring sequences lie as many indices as the rows can touch blocks,
+    whatever the first position."""
+    for lo in list(range(0, 130)) + [10 ** 6 + 63]:
+        for count in list(range(0, 200)) + [4095, 4096, 4097]:
+            room = rows.base(lo + count, 8) - rows.base(lo, 7)
+            assert room >= (count + 62) // 64 + 1
+            if count:
+                assert max(len(_tiles(rows, 1, lo, lo + count, 7, 1 << 30, count, s + count, 1 << 20, 1 << 30))
+                           for s in (0, 1, 62, 63)) <= min(room, rows.max_tiles(count))
 
 
 @pytest.mark.parametrize("args,bad", [

@@ -10,13 +10,23 @@
 // codes' subnormals. Norm, rotation and the division are in fp32; each value
 // is rounded once.
 //
-// One launch: the first CTAs take the query heads (four heads of a token for
-// each row slot, head_row.cuh), the others one (sequence, block, KV head) of
-// K or of V each, so that the rows of a page that is new to this call are read
-// and written once, its amax needs no second pass, and no two CTAs share a
-// scale. Bound by HBM for prompts, by the launch for single tokens.
+// One launch, of one of two kernels. Single tokens (max_new = 1) are bound by latency:
+// a row slot (the D / 16 lanes of a row, head_row.cuh) takes one query head, a
+// warp the new row of one (sequence, KV head) of K or of V. Prompts are bound by HBM:
+// persistent CTAs take (sequence, block, KV head) tiles of K and of V, so that new
+// rows are read and written once, their amax needs no second pass and no two
+// CTAs share a scale, and units of four query heads; each thread prefetches its
+// pieces of the next tile or unit with cp.async.
+//
+// Measured on one B200 (32/8 heads of 128): one token of one sequence 3.8 us (8.3
+// with a CTA's 64-row tile for it), of 64 sequences into 8-bit pages 7.4 us, two
+// of which fill a page, of 256 sequences 9.2 (22.5); prompts of 8k and 32k tokens
+// into bf16 pages 43 and 147 us (74 and 86% of the copy rate; 45 and 170 with one
+// CTA for each tile and four heads' loads in registers), 8k into 8-bit pages 43.8.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "head_row.cuh"
 #include "launch.h"
@@ -24,8 +34,6 @@
 
 namespace sas {
 namespace {
-
-constexpr int kThreads = 128;
 
 using bf16 = __nv_bfloat16;
 
@@ -46,54 +54,13 @@ __device__ __forceinline__ int seq_of_row(const AppendArgs& a, long long t) {
     return __ldg(a.cu_new + lo) <= t && t < __ldg(a.cu_new + lo + 1) ? lo : -1;
 }
 
-constexpr int kHeads = 4;       // query heads of one token that a row slot takes
-
-template <int D>
-__device__ __forceinline__ void append_q(const AppendArgs& a, uint32_t cta) {
-    constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
-    const int l = threadIdx.x % HeadRow<D>::kLanes;
-    const uint32_t parts = ((uint32_t)a.Hq + kHeads - 1) / kHeads;
-    const uint32_t u = cta * kSlots + threadIdx.x / HeadRow<D>::kLanes, t = u / parts, h0 = u - t * parts;
-    // the rows' loads are on their way before the token's sequence is looked for
-    const bf16* src = static_cast<const bf16*>(a.q) + (t < a.T ? t * a.ld_q : 0) + 8 * l;
-    uint4 lo[kHeads][1], hi[kHeads][1];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = (int)(h0 + i * parts);
-        lo[i][0] = hi[i][0] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < a.T && h < a.Hq) {
-            lo[i][0] = ld_stream(src + h * D);
-            hi[i][0] = ld_stream(src + h * D + D / 2);
-        }
-    }
-    const bf16* weight = static_cast<const bf16*>(a.q_weight);
-    const Row w = load_weight<bf16, D>(weight, l);
-    // -1: a padding entry, whose row is zero; rows of no sequence, or of one that is skipped, stay as they are
-    int pos = -1;
-    bool live = t < a.T;
-    if (live) {
-        const int n = seq_of_row(a, t);
-        live = n >= 0;
-        if (live) {
-            const SeqNew s = load_seq(a, n);
-            live = !s.bad;
-            if (s.count > 0) pos = s.first + (int)(t - s.row0);
-        }
-    }
-    const Turn turn(load_angles<bf16, D>(a.table, live ? max(pos, 0) : 0, l), w);
-    bf16* dst = static_cast<bf16*>(a.q_out) + (long long)t * a.Hq * D;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = (int)(h0 + i * parts);
-        Row x;
-        x.a = Raw8<bf16>::get(lo[i]);
-        x.b = Raw8<bf16>::get(hi[i]);
-        Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
-        if (pos < 0) y.a = y.b = Half{};
-        if (live && h < a.Hq) {
-            store_row<D>(dst + h * D, l, y);
-        }
-    }
+// Position of token row t: -1 for a padding entry, whose rows are zero; -2 for rows
+// of no sequence, or of one that is skipped, which stay as they are.
+__device__ __forceinline__ int append_pos(const AppendArgs& a, long long t) {
+    const int n = seq_of_row(a, t);
+    if (n < 0) return -2;
+    const SeqNew s = load_seq(a, n);
+    return s.bad ? -2 : s.count > 0 ? s.first + (int)(t - s.row0) : -1;
 }
 
 // Eight e4m3 codes (8 bytes) from eight values times inv, and back.
@@ -119,119 +86,411 @@ __device__ __forceinline__ void add(Half& s, const Half& x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) s.v[i] = f2_add(s.v[i], x.v[i]);
 }
-// An infinity has no code: it is kept as NaN. Returns the largest finite magnitude so far.
-__device__ __forceinline__ float finite_max(Half& x, float m) {
+// Largest magnitude of a row's values (NaN ignored) and m.
+__device__ __forceinline__ float row_max(const Row& x, float m) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 f = f2_unpack(x.v[i]);
-        if (!(fabsf(f.x) <= 3.402823466e38f)) f.x = __int_as_float(0x7fffffff);
-        if (!(fabsf(f.y) <= 3.402823466e38f)) f.y = __int_as_float(0x7fffffff);
-        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-        x.v[i] = f2_pack(f.x, f.y);
+        const float2 f = f2_unpack(x.a.v[i]), g = f2_unpack(x.b.v[i]);
+        m = sm100::max3(m, fabsf(f.x), fabsf(f.y));
+        m = sm100::max3(m, fabsf(g.x), fabsf(g.y));
     }
     return m;
 }
+// An infinity has no code: it is kept as NaN.
+__device__ __forceinline__ void drop_infinities(Half& x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f = f2_unpack(x.v[i]);
+        if (fabsf(f.x) == INFINITY) f.x = __int_as_float(0x7fffffff);
+        if (fabsf(f.y) == INFINITY) f.y = __int_as_float(0x7fffffff);
+        x.v[i] = f2_pack(f.x, f.y);
+    }
+}
 
+// A row slot's fp32 sums to a row of shared memory.
+template <int D>
+__device__ __forceinline__ void store_sum(float* p, int l, const Row& x) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<ulonglong2*>(p + 8 * l + 4 * i) = make_ulonglong2(x.a.v[2 * i], x.a.v[2 * i + 1]);
+        *reinterpret_cast<ulonglong2*>(p + D / 2 + 8 * l + 4 * i) = make_ulonglong2(x.b.v[2 * i], x.b.v[2 * i + 1]);
+    }
+}
+
+// The scale of a page and head with new rows of magnitude up to m: the old one
+// (`lo` rows are there already) where it holds them.
+struct PageScale {
+    bool ok, keep;
+    float s;
+};
+__device__ __forceinline__ PageScale page_scale(int lo, float old, float m) {
+    PageScale p;
+    p.ok = lo == 0 || scale_ok(old);        // else the rows already there have no value
+    p.keep = lo > 0 && m <= 448.f * old;
+    p.s = p.keep ? old : __int_as_float((scale_exp(__float_as_uint(m)) + 127) << 23);
+    return p;
+}
+
+// The mean key of a filled page is summed in one order by both kernels: the
+// rows j, j + kSumRows, ... for each j, then these sums by j.
+template <int D>
+constexpr int kSumRows = D == 128 ? 16 : 32;
+
+// ------------------------------------------------------------------ single tokens
+constexpr int kTokenThreads = 128;
+
+template <int D>
+__device__ __forceinline__ void token_q(const AppendArgs& a, uint32_t u) {
+    const int l = threadIdx.x % HeadRow<D>::kLanes;
+    const uint32_t t = u / (uint32_t)a.Hq, h = u - t * a.Hq;
+    const bool in = t < a.T;
+    // the row's loads are on their way before the token's sequence is looked for
+    const bf16* src = static_cast<const bf16*>(a.q) + (in ? t * a.ld_q + h * D : 0) + 8 * l;
+    uint4 lo[1] = {make_uint4(0u, 0u, 0u, 0u)}, hi[1] = {lo[0]};
+    if (in) lo[0] = ld_stream(src), hi[0] = ld_stream(src + D / 2);
+    const bf16* weight = static_cast<const bf16*>(a.q_weight);
+    const Row w = load_weight<bf16, D>(weight, l);
+    const int pos = in ? append_pos(a, t) : -2;
+    const Turn turn(load_angles<bf16, D>(a.table, max(pos, 0), l), w);
+    const Row x = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
+    Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+    if (pos < 0) y = Row{};
+    if (pos > -2) store_row<D>(static_cast<bf16*>(a.q_out) + (long long)u * D, l, y);
+}
+
+// The new row of one (sequence, KV head) of K or of V, by one warp: its first
+// D / 16 lanes hold the row, the whole warp does the rare work on the page's
+// older rows. `red`: the warp's [kSumRows][D] floats.
 template <int D, bool kQ8>
-__device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
-    __shared__ __align__(16) float red[kSlots][D];
-    __shared__ float wmax[kThreads / 32];
-    const int tiles = max_tiles(a.max_new);
-    const int h = (int)(item % a.Hkv);
-    const bool is_v = (item / a.Hkv) & 1;
-    const long long nt = item / (2 * a.Hkv);
-    const int n = (int)(nt / tiles);
-    const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-    const SeqNew s = load_seq(a, n);
+__device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float (*red)[D]) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
+    if (u >= 2u * a.N * a.Hkv) return;
+    const uint32_t n = u / (2u * a.Hkv), rest = u - n * 2u * a.Hkv;
+    const bool is_v = rest >= (uint32_t)a.Hkv;
+    const int h = (int)(is_v ? rest - a.Hkv : rest);
+    const SeqNew s = load_seq(a, (int)n);
+    bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
     if (s.bad) {
-        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+        if (lane == 0) flag_status(a.status, kStatusBadData);
         return;
     }
-    bf16* k_out = static_cast<bf16*>(a.k_out);
-    if (s.count == 0 && a.cu_new == nullptr && k_out != nullptr && !is_v && slot == 0) {   // a padding entry
-        store_row<D>(k_out + ((long long)n * a.Hkv + h) * D, l, Row{});
+    if (s.count == 0) {
+        if (a.cu_new == nullptr && k_out != nullptr && grp == 0)       // a padding entry
+            store_row<D>(k_out + ((long long)n * a.Hkv + h) * D, l, Row{});
+        return;
     }
-    const PageTile t = page_tile(s, (int)(nt % tiles));
-    if (t.hi <= t.lo) return;
-    const int page = __ldg(a.page_table + (long long)n * a.max_pages + t.block);    // block < max_pages by kv_len's check
-    const bool page_ok = page >= 0 && page < a.num_pages;
-    if (!page_ok) {
-        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-        if (is_v || k_out == nullptr) return;
+    const PageTile t = page_tile(s, 0);             // the one new row is t.lo
+    const int page = __ldg(a.page_table + (long long)n * a.max_pages + t.block);   // block < max_pages by kv_len's check
+    const bf16* src = (is_v ? static_cast<const bf16*>(a.v) + t.row * a.ld_v : static_cast<const bf16*>(a.k) + t.row * a.ld_k) +
+                      h * D + 8 * l;
+    const uint4 lo[1] = {ld_stream(src)}, hi[1] = {ld_stream(src + D / 2)};
+    const bf16* weight = static_cast<const bf16*>(a.k_weight);
+    const Row w = load_weight<bf16, D>(weight, l);
+    const Angles ang = load_angles<bf16, D>(a.table, s.first, l);
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok && lane == 0) flag_status(a.status, kStatusBadData);
+    const long long tile0 = ok ? ((long long)page * a.Hkv + h) * kPageRows : 0;     // row of the cache
+    float* scale = kQ8 ? (is_v ? a.v_scale : a.k_scale) + (ok ? (long long)page * a.Hkv + h : 0) : nullptr;
+    const float old = kQ8 && ok && t.lo > 0 ? *scale : 0.f;
+
+    Row x = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
+    if (!is_v) {
+        x = norm_turn(x, w, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f, ang);
+        if (k_out != nullptr && grp == 0) store_row<D>(k_out + (t.row * a.Hkv + h) * D, l, x);
+    }
+    if (!ok) return;
+
+    PageScale ps{true, true, 1.f};
+    if constexpr (kQ8) {
+        float m = warp_max(row_max(x, 0.f));        // (behind the shuffles every lane has read the old scale)
+        if (m == INFINITY) {
+            drop_infinities(x.a);
+            drop_infinities(x.b);
+            m = warp_max(row_max(x, 0.f));
+        }
+        ps = page_scale(t.lo, old, m);
+        if (!ps.ok) {
+            if (lane == 0) flag_status(a.status, kStatusBadData);
+            return;
+        }
+        if (grp == 0) {
+            uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (tile0 + t.lo) * D;
+            *reinterpret_cast<uint2*>(row + 8 * l) = to_codes(x.a, 1.f / ps.s);
+            *reinterpret_cast<uint2*>(row + D / 2 + 8 * l) = to_codes(x.b, 1.f / ps.s);
+        }
+        if (lane == 0 && !ps.keep) *scale = ps.s;
+    } else if (grp == 0) {
+        store_row<D>(static_cast<bf16*>(is_v ? a.v_cache : a.k_cache) + (tile0 + t.lo) * D, l, x);
     }
 
-    // the new rows, one for each of kRows steps of a slot
-    const bf16* src = (is_v ? static_cast<const bf16*>(a.v) : static_cast<const bf16*>(a.k)) + h * D + 8 * l;
-    const long long ld = is_v ? a.ld_v : a.ld_k;
-    uint4 lo[kRows][1], hi[kRows][1];
+    const bool grown = kQ8 && t.lo > 0 && !ps.keep, pool = !is_v && a.kpool != nullptr && t.lo == kPageRows - 1;
+    if (!grown && !pool) return;
+    __syncwarp();                                   // the new row is written
+    const float ratio = old * (1.f / ps.s);
+    const int rows = t.lo + pool;                   // with pool the new row is read back with the others
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = slot + i * kSlots;
-        lo[i][0] = hi[i][0] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= t.lo && r < t.hi) {
-            const bf16* p = src + (t.row + r - t.lo) * ld;
-            lo[i][0] = ld_stream(p);
-            hi[i][0] = ld_stream(p + D / 2);
+    for (int k = 0; k < kSumRows<D> / kPerWarp; ++k) {
+        Row sum{};
+#pragma unroll
+        for (int i = 0; i < kPageRows / kSumRows<D>; ++i) {
+            const int r = grp + kPerWarp * k + kSumRows<D> * i;
+            if (r >= rows) continue;
+            if (kQ8) {
+                uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (tile0 + r) * D + 8 * l;
+                uint2 c = *reinterpret_cast<const uint2*>(row), c2 = *reinterpret_cast<const uint2*>(row + D / 2);
+                if (grown && r < t.lo) {
+                    *reinterpret_cast<uint2*>(row) = c = to_codes(from_codes(c), ratio);
+                    *reinterpret_cast<uint2*>(row + D / 2) = c2 = to_codes(from_codes(c2), ratio);
+                }
+                if (pool) {
+                    add(sum.a, from_codes(c));
+                    add(sum.b, from_codes(c2));
+                }
+            } else {
+                const bf16* row = static_cast<const bf16*>(a.k_cache) + (tile0 + r) * D + 8 * l;
+                const uint4 c[1] = {*reinterpret_cast<const uint4*>(row)}, c2[1] = {*reinterpret_cast<const uint4*>(row + D / 2)};
+                add(sum.a, Raw8<bf16>::get(c));
+                add(sum.b, Raw8<bf16>::get(c2));
+            }
+        }
+        if (pool) store_sum<D>(red[grp + kPerWarp * k], l, sum);
+    }
+    if (!pool) return;
+    __syncwarp();
+    for (int d = lane; d < D; d += 32) {
+        float m = 0.f;
+#pragma unroll 16
+        for (int i = 0; i < kSumRows<D>; ++i) m += red[i][d];
+        a.kpool[((long long)page * a.Hkv + h) * D + d] = m * ps.s * (1.f / kPageRows);
+    }
+}
+
+template <int D, bool kQ8>
+__global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const AppendArgs a, uint32_t q_ctas) {
+    constexpr int kSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
+    __shared__ __align__(16) float red[kCtaWarps][kSumRows<D>][D];
+    if (blockIdx.x < q_ctas)
+        token_q<D>(a, blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes);
+    else
+        token_kv<D, kQ8>(a, (blockIdx.x - q_ctas) * kCtaWarps + threadIdx.x / 32, red[threadIdx.x / 32]);
+}
+
+// ------------------------------------------------------------------ prompts
+constexpr int kThreads = 128;
+constexpr int kHeads = 4;                   // query heads of a unit
+constexpr int kCtas = 4;                    // resident CTAs of an SM
+constexpr int kStages = 2;                  // pieces of work in flight
+constexpr int kStageBytes = 2 * kHeads * kThreads * 16;    // a thread's pieces of a unit, or of its rows of a tile
+
+// A piece of work of a CTA: a (sequence, block, KV head) tile of K or of V with new
+// rows, or a query unit for each of its row slots, in few registers: one waits while
+// the other is worked on.
+struct Work {
+    enum : uint32_t { kNone, kUnit, kK, kV };
+    uint32_t kind;          // bits 0-1; of a tile: rows lo (bits 8-15) to hi (bits 16-23)
+    int at;                 // a unit: its number; a tile: the token row of its first new row
+    int pos;                // a unit: its position (append_pos); a tile: its block
+    int h, page;            // a tile's KV head and page
+    __device__ __forceinline__ bool is(uint32_t k) const { return (kind & 3) == k; }
+    __device__ __forceinline__ bool tile() const { return kind & 2; }
+    __device__ __forceinline__ int lo() const { return kind >> 8 & 255; }
+    __device__ __forceinline__ int hi() const { return kind >> 16; }
+};
+// The sequence that a thread's last piece of work belonged to. The next one mostly
+// belongs to it too, and then no load stands in front of its copies.
+struct SeqAt {
+    int n = -1;                 // -1: none yet
+    int row0 = 0, count = 0, first = 0;
+    uint32_t tile0 = 0, tile1 = 0;      // its tile indices (seq_tile_base)
+    bool bad = false;
+    __device__ __forceinline__ void load(const AppendArgs& a, int at) {
+        const SeqNew s = load_seq(a, at);
+        n = at;
+        row0 = (int)s.row0;
+        count = s.count;
+        first = s.first;
+        bad = s.bad;
+        tile0 = seq_tile_base(__ldg(a.cu_new + at), at);
+        tile1 = seq_tile_base(__ldg(a.cu_new + at + 1), at + 1);
+    }
+};
+__device__ __forceinline__ Work kv_work(const AppendArgs& a, SeqAt& s, uint32_t v, uint32_t rest) {
+    Work k{};
+    const bool is_v = rest >= (uint32_t)a.Hkv;
+    if (s.n < 0 || v < s.tile0 || v >= s.tile1) {       // the last n with its tile base <= v
+        int lo = 0, hi = a.N;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (seq_tile_base(__ldg(a.cu_new + mid), mid) <= v) lo = mid; else hi = mid;
+        }
+        s.load(a, lo);
+    }
+    if (s.bad || v < s.tile0 || v - s.tile0 >= (uint32_t)max_tiles(a.max_new)) return k;
+    const PageTile t = page_tile(SeqNew{s.row0, s.first, s.count, false}, (int)(v - s.tile0));
+    if (t.hi <= t.lo) return k;
+    k.kind = (is_v ? Work::kV : Work::kK) | (uint32_t)t.lo << 8 | (uint32_t)t.hi << 16;
+    k.at = (int)t.row;
+    k.pos = t.block;
+    k.h = (int)(is_v ? rest - a.Hkv : rest);
+    k.page = __ldg(a.page_table + (long long)s.n * a.max_pages + t.block);     // block < max_pages by kv_len's check
+    return k;
+}
+template <int D>
+__device__ __forceinline__ Work q_work(const AppendArgs& a, SeqAt& s, uint32_t batch, uint32_t q_units) {
+    Work k{};
+    k.kind = Work::kUnit;
+    k.pos = -2;
+    const uint32_t u = batch * (kThreads / HeadRow<D>::kLanes) + threadIdx.x / HeadRow<D>::kLanes;
+    if (u < q_units) {
+        const int t = (int)(u / parts_of(a.Hq, kHeads));
+        if (s.n < 0 || s.bad || t < s.row0 || t - s.row0 >= s.count) {
+            const int n = seq_of_row(a, t);
+            if (n >= 0) s.load(a, n);
+        }
+        k.at = (int)u;
+        if (s.n >= 0 && !s.bad && t >= s.row0 && t - s.row0 < s.count) k.pos = s.first + (t - s.row0);
+    }
+    return k;
+}
+
+// Starts the copies of a piece of work into a stage.
+template <int D>
+__device__ __forceinline__ void issue(const AppendArgs& a, const Work& k, uint32_t at) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
+    const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+    if (k.tile()) {
+        const bool is_v = k.is(Work::kV);
+        const bf16* src = (is_v ? static_cast<const bf16*>(a.v) : static_cast<const bf16*>(a.k)) + k.h * D;
+        const long long ld = is_v ? a.ld_v : a.ld_k;
+        const int lo = k.lo(), hi = k.hi();
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = slot + i * kSlots;        // rows that are not new: zeroes, copied from nowhere
+            copy_row<bf16, D, kThreads>(at + 2 * i * kThreads * 16, src + (k.at + min(max(r, lo), hi - 1) - lo) * ld, l,
+                                        r >= lo && r < hi);
+        }
+    } else if (k.is(Work::kUnit) && k.pos > -2) {
+        const uint32_t parts = parts_of(a.Hq, kHeads), t = k.at / parts;
+        const bf16* src = static_cast<const bf16*>(a.q) + (long long)t * a.ld_q;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = (int)(k.at - t * parts + i * parts);
+            copy_row<bf16, D, kThreads>(at + 2 * i * kThreads * 16, src + (h < a.Hq ? h : 0) * D, l, h < a.Hq);
         }
     }
+    copy_commit();
+}
+
+template <int D>
+__device__ __forceinline__ void store_unit(const AppendArgs& a, const Work& k, uint32_t at) {
+    const int l = threadIdx.x % HeadRow<D>::kLanes;
+    const bf16* weight = static_cast<const bf16*>(a.q_weight);
+    const uint32_t parts = parts_of(a.Hq, kHeads), t = k.at / parts;
+    const Turn turn(load_angles<bf16, D>(a.table, max(k.pos, 0), l), load_weight<bf16, D>(weight, l));
+    bf16* dst = static_cast<bf16*>(a.q_out) + (long long)t * a.Hq * D;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int h = (int)(k.at - t * parts + i * parts);
+        const Row x = read_row<bf16, kThreads>(at + 2 * i * kThreads * 16);
+        Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+        if (k.pos < 0) y = Row{};
+        if (k.pos > -2 && h < a.Hq) store_row<D>(dst + h * D, l, y);
+    }
+}
+
+// `stage`: the CTA's whole stage of this tile, `at` this thread's pieces of it.
+template <int D, bool kQ8>
+__device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, uint32_t at, uint8_t* stage, float* wmax) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
+    const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, lo = k.lo(), hi = k.hi();
+    const bool is_v = k.is(Work::kV), page_ok = k.page >= 0 && k.page < a.num_pages;
+    bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
+    if (!page_ok) {
+        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+        if (k_out == nullptr) return;
+    }
+    const long long tile0 = page_ok ? ((long long)k.page * a.Hkv + k.h) * kPageRows : 0;      // row of the cache
+    float* scale = kQ8 ? (is_v ? a.v_scale : a.k_scale) + (page_ok ? (long long)k.page * a.Hkv + k.h : 0) : nullptr;
+    const float old = kQ8 && page_ok && lo > 0 ? *scale : 0.f;
+    if (!kQ8 && is_v) {             // values into bf16 pages: as they are
+        bf16* cache = static_cast<bf16*>(a.v_cache) + tile0 * D + 8 * l;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = slot + i * kSlots;
+            if (r < lo || r >= hi) continue;
+            *reinterpret_cast<uint4*>(cache + r * D) = ld_shared16(at + 2 * i * kThreads * 16);
+            *reinterpret_cast<uint4*>(cache + r * D + D / 2) = ld_shared16(at + (2 * i + 1) * kThreads * 16);
+        }
+        return;
+    }
     const bf16* weight = static_cast<const bf16*>(a.k_weight);
-    Row w;
-    if (!is_v) w = load_weight<bf16, D>(weight, l);
     Row x[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        x[i].a = Raw8<bf16>::get(lo[i]);
-        x[i].b = Raw8<bf16>::get(hi[i]);
-        if (is_v) continue;
         const int r = slot + i * kSlots;
+        x[i] = read_row<bf16, kThreads>(at + 2 * i * kThreads * 16);
+        if (is_v) continue;
         const float rr = weight != nullptr ? row_rrms<D>(x[i], a.eps) : 1.f;
-        if (r >= t.lo && r < t.hi) {
-            x[i] = Turn(load_angles<bf16, D>(a.table, t.block * kPageRows + r, l), w)(x[i], rr);
-            if (k_out != nullptr) store_row<D>(k_out + ((t.row + r - t.lo) * a.Hkv + h) * D, l, x[i]);
+        x[i] = norm_turn(x[i], load_weight<bf16, D>(weight, l), rr,
+                         load_angles<bf16, D>(a.table, k.pos * kPageRows + min(max(r, lo), hi - 1), l));
+        if (r < lo || r >= hi) {
+            x[i] = Row{};               // not a new row: nothing of it counts
+        } else {
+            if (k_out != nullptr) store_row<D>(k_out + ((long long)(k.at + r - lo) * a.Hkv + k.h) * D, l, x[i]);
+            if (!kQ8 && page_ok) store_row<D>(static_cast<bf16*>(a.k_cache) + (tile0 + r) * D, l, x[i]);
         }
     }
     if (!page_ok) return;
-    const long long tile0 = ((long long)page * a.Hkv + h) * kPageRows;      // row of the cache
-    const bool pool = a.kpool != nullptr && !is_v && t.hi == kPageRows;
+    const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows;
     Row sum{};
     float unit = 1.f;               // what a pooled value is in
 
     if constexpr (kQ8) {
         uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D + 8 * l;
-        float* scale = (is_v ? a.v_scale : a.k_scale) + (long long)page * a.Hkv + h;
-        const float old = t.lo > 0 ? *scale : 0.f;
-        float m = 0.f;              // rows that are not new are zero here
+        auto tile_max = [&] {
+            float m = 0.f;              // rows that are not new are zero here
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) m = finite_max(x[i].b, finite_max(x[i].a, m));
-        m = warp_max(m);
-        if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-        __syncthreads();            // (and every thread has read the old scale)
+            for (int i = 0; i < kRows; ++i) m = row_max(x[i], m);
+            m = warp_max(m);
+            __syncthreads();            // the last maxima have been read
+            if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
+            __syncthreads();            // (and every thread has read the old scale)
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
-        if (t.lo > 0 && !scale_ok(old)) {       // the rows already there have no value
+            for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
+            return m;
+        };
+        float m = tile_max();
+        if (m == INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                drop_infinities(x[i].a);
+                drop_infinities(x[i].b);
+            }
+            m = tile_max();
+        }
+        const PageScale ps = page_scale(lo, old, m);
+        if (!ps.ok) {
             if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
             return;
         }
-        const bool keep = t.lo > 0 && m <= 448.f * old;
-        const float sn = keep ? old : __int_as_float((scale_exp(__float_as_uint(m)) + 127) << 23);
-        const float inv = 1.f / sn, ratio = old * inv;
-        if (threadIdx.x == 0 && !keep) *scale = sn;
-        unit = sn;
+        const float inv = 1.f / ps.s, ratio = old * inv;
+        if (threadIdx.x == 0 && !ps.keep) *scale = ps.s;
+        unit = ps.s;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = slot + i * kSlots;
-            if (r >= t.hi || (r < t.lo && keep && !pool)) continue;
+            if (r >= hi || (r < lo && ps.keep && !pool)) continue;
             uint2* p = reinterpret_cast<uint2*>(cache + r * D);
             uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2);
             uint2 c, c2;
-            if (r >= t.lo) {
+            if (r >= lo) {
                 *p = c = to_codes(x[i].a, inv);
                 *p2 = c2 = to_codes(x[i].b, inv);
             } else {
                 c = *p;
                 c2 = *p2;
-                if (!keep) {
+                if (!ps.keep) {
                     *p = c = to_codes(from_codes(c), ratio);
                     *p2 = c2 = to_codes(from_codes(c2), ratio);
                 }
@@ -242,53 +501,114 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, long long item) {
             }
         }
     } else {
-        bf16* cache = static_cast<bf16*>(is_v ? a.v_cache : a.k_cache) + tile0 * D;
+        if (!pool) return;
+        const bf16* cache = static_cast<const bf16*>(a.k_cache) + tile0 * D + 8 * l;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = slot + i * kSlots;
-            if (r >= t.lo && r < t.hi) store_row<D>(cache + r * D, l, x[i]);
-            if (pool) {             // what this thread has stored, or an older row
-                const bf16* p = cache + r * D + 8 * l;
-                const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)}, v[1] = {*reinterpret_cast<const uint4*>(p + D / 2)};
-                add(sum.a, Raw8<bf16>::get(u));
-                add(sum.b, Raw8<bf16>::get(v));
-            }
+        for (int i = 0; i < kRows; ++i) {           // what this thread has stored, and older rows
+            const bf16* p = cache + (slot + i * kSlots) * D;
+            const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)}, v[1] = {*reinterpret_cast<const uint4*>(p + D / 2)};
+            add(sum.a, Raw8<bf16>::get(u));
+            add(sum.b, Raw8<bf16>::get(v));
         }
     }
     if (!pool) return;
-    // the filled page's mean key: the slots' sums in slot order
-    *reinterpret_cast<ulonglong2*>(&red[slot][8 * l]) = make_ulonglong2(sum.a.v[0], sum.a.v[1]);
-    *reinterpret_cast<ulonglong2*>(&red[slot][8 * l + 4]) = make_ulonglong2(sum.a.v[2], sum.a.v[3]);
-    *reinterpret_cast<ulonglong2*>(&red[slot][D / 2 + 8 * l]) = make_ulonglong2(sum.b.v[0], sum.b.v[1]);
-    *reinterpret_cast<ulonglong2*>(&red[slot][D / 2 + 8 * l + 4]) = make_ulonglong2(sum.b.v[2], sum.b.v[3]);
+    // the filled page's mean key: the slots' sums in slot order, where the rows were
+    static_assert(kSlots == kSumRows<D> && kSlots * D * 4 <= kStageBytes, "sums of a tile");
+    float(*red)[D] = reinterpret_cast<float(*)[D]>(stage);
+    __syncthreads();                // every thread has its rows
+    store_sum<D>(red[slot], l, sum);
     __syncthreads();
     if (threadIdx.x < D) {
         float m = 0.f;
+#pragma unroll 16
         for (int i = 0; i < kSlots; ++i) m += red[i][threadIdx.x];
-        a.kpool[((long long)page * a.Hkv + h) * D + threadIdx.x] = m * unit * (1.f / kPageRows);
+        a.kpool[((long long)k.page * a.Hkv + k.h) * D + threadIdx.x] = m * unit * (1.f / kPageRows);
     }
+    __syncthreads();                // read before the stage's next copies
 }
 
+// A CTA's share: batches of query units (kSlots units each) and tiles, contiguous
+// runs of both (neighbouring tiles are the heads of one block, whose table rows
+// are then L1 hits; every gridDim-th tile instead takes 2 to 10% longer). It starts with a
+// batch of units, whose copies wait for no lookup.
 template <int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, long long q_ctas) {
-    if (blockIdx.x < q_ctas)
-        append_q<D>(a, blockIdx.x);
-    else
-        append_kv<D, kQ8>(a, blockIdx.x - q_ctas);
+__global__ void __launch_bounds__(kThreads, kCtas)
+append_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t items) {
+    constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
+    __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
+    __shared__ float wmax[kThreads / 32];
+    const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
+    // both kinds in proportion, their sum to within one: where a CTA has a batch at least, all shares are >= 0
+    const uint32_t c = blockIdx.x;
+    auto share = [&](unsigned long long n, uint32_t c) { return (uint32_t)(n * c / gridDim.x); };
+    const unsigned long long all = (unsigned long long)batches + items;
+    uint32_t kv0 = share(items, c), kv1 = share(items, c + 1), q0 = share(all, c) - kv0, q1 = share(all, c + 1) - kv1;
+    if (batches < gridDim.x) {          // few batches: one list, the batches first
+        const uint32_t b0 = share(all, c), b1 = share(all, c + 1);
+        q0 = min(b0, batches), q1 = min(b1, batches);
+        kv0 = max(b0, batches) - batches, kv1 = max(b1, batches) - batches;
+    }
+    const uint32_t lead = q1 > q0 ? 1 : 0, tiles = kv1 - kv0, count = q1 - q0 + tiles;
+    static_assert(kStages == 2, "one piece of work waits");
+    SeqAt seq;
+    uint32_t v = kv0 / (2u * a.Hkv), rest = kv0 - v * 2u * a.Hkv;       // the next tile: its index, and head of K or of V
+    auto work_at = [&](uint32_t j) {
+        if (j >= lead && j < lead + tiles) {
+            const Work k = kv_work(a, seq, v, rest);
+            if (++rest == 2u * a.Hkv) rest = 0, ++v;
+            return k;
+        }
+        return q_work<D>(a, seq, q0 + (j < lead ? j : j - tiles), j < count ? q_units : 0);
+    };
+    Work cur = work_at(0);
+    issue<D>(a, cur, ring);
+    uint32_t st = 0;
+    for (uint32_t j = 0; j < count; ++j) {
+        const Work next = work_at(j + 1);
+        issue<D>(a, next, ring + (st ^ 1) * kStageBytes);
+        copy_wait<kStages - 1>();
+        if (cur.tile())
+            store_tile<D, kQ8>(a, cur, ring + st * kStageBytes, ring_s + st * kStageBytes, wmax);
+        else if (cur.is(Work::kUnit))
+            store_unit<D>(a, cur, ring + st * kStageBytes);
+        cur = next;
+        st ^= 1;
+    }
+    copy_wait<0>();
+    // every sequence that breaks the call's terms, also those that no tile index leads to
+    if (blockIdx.x == 0)
+        for (int n = threadIdx.x; n < a.N; n += kThreads)
+            if (load_seq(a, n).bad || __ldg(a.cu_new + n + 1) < __ldg(a.cu_new + n)) flag_status(a.status, kStatusBadData);
 }
 
 template <int D, bool kQ8>
 cudaError_t go(const AppendArgs& a, cudaStream_t st) {
-    constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
-    const long long q_ctas = a.q != nullptr ? (a.T * ((a.Hq + kHeads - 1) / kHeads) + kSlots - 1) / kSlots : 0;
-    append_kernel<D, kQ8><<<(unsigned)(q_ctas + append_kv_ctas(a)), kThreads, 0, st>>>(a, q_ctas);
+    constexpr long long kSlots = kThreads / HeadRow<D>::kLanes;
+    const long long items = append_items(a);
+    if (a.max_new == 1) {
+        constexpr long long kTokenSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
+        const long long q_ctas = a.q != nullptr ? (a.T * a.Hq + kTokenSlots - 1) / kTokenSlots : 0;
+        append_token_kernel<D, kQ8>
+            <<<(unsigned)(q_ctas + (items + kCtaWarps - 1) / kCtaWarps), kTokenThreads, 0, st>>>(a, (uint32_t)q_ctas);
+    } else {
+        int dev = 0, sms = 148;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            sms = 148;
+        const long long q_units = a.q != nullptr ? a.T * parts_of(a.Hq, kHeads) : 0;
+        const long long batches = (q_units + kSlots - 1) / kSlots, most = (long long)kCtas * sms;
+        append_kernel<D, kQ8><<<(unsigned)std::min(batches + items, most), kThreads, 0, st>>>(
+            a, (uint32_t)q_units, (uint32_t)batches, (uint32_t)items);
+    }
     count_launches(1);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-long long append_kv_ctas(const AppendArgs& a) { return (long long)a.N * max_tiles(a.max_new) * a.Hkv * 2; }
+long long append_items(const AppendArgs& a) {
+    return (a.max_new == 1 ? (long long)a.N : (long long)seq_tile_base((int)a.T, a.N) + 1) * a.Hkv * 2;
+}
 
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t st) {
     if (a.k_scale != nullptr) return D == 128 ? go<128, true>(a, st) : go<64, true>(a, st);

@@ -193,6 +193,19 @@ struct Turn {
     }
 };
 
+// One row alone, with the weights at hand: n = x (w r), then the turn.
+__device__ __forceinline__ Row norm_turn(const Row& x, const Row& w, float r, const Angles& g) {
+    const f2 rr = f2_pack(r, r), neg = f2_pack(-1.f, -1.f);
+    Row y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f2 a = f2_mul(x.a.v[i], f2_mul(w.a.v[i], rr)), b = f2_mul(x.b.v[i], f2_mul(w.b.v[i], rr));
+        y.a.v[i] = f2_fma(a, g.c.v[i], f2_mul(b, f2_mul(g.s.v[i], neg)));
+        y.b.v[i] = f2_fma(b, g.c.v[i], f2_mul(a, g.s.v[i]));
+    }
+    return y;
+}
+
 // 16 bytes from global to shared memory without a register (zeroes without
 // `live`); each thread copies and later reads its own pieces only, so that the
 // groups need no barrier.
@@ -212,5 +225,28 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t p) {
                  : "memory");
     return w;
 }
+
+// A head row of a thread's pieces: copy from global memory (src: the row), and
+// read. From half to half: kPieces * kThreads * 16 bytes.
+template <typename T, int D, int kThreads>
+__device__ __forceinline__ void copy_row(uint32_t at, const T* src, int l, bool live) {
+    constexpr int kP = Raw8<T>::kPieces;
+#pragma unroll
+    for (int i = 0; i < 2 * kP; ++i)
+        copy16(at + i * kThreads * 16, src + i / kP * (D / 2) + i % kP * (D / 4) + Raw8<T>::kStep * l, live);
+}
+template <typename T, int kThreads>
+__device__ __forceinline__ Row read_row(uint32_t at) {
+    constexpr int kP = Raw8<T>::kPieces;
+    uint4 p[kP], q[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+        p[i] = ld_shared16(at + i * kThreads * 16);
+        q[i] = ld_shared16(at + (kP + i) * kThreads * 16);
+    }
+    return {Raw8<T>::get(p), Raw8<T>::get(q)};
+}
+
+__host__ __device__ __forceinline__ uint32_t parts_of(int H, int heads) { return ((uint32_t)H + heads - 1) / heads; }
 
 }  // namespace sas

@@ -50,34 +50,12 @@ struct Bwd {
     static constexpr int kSmem = kRing > kSlots * D * 4 ? kRing : kSlots * D * 4;
 };
 
-__host__ __device__ __forceinline__ uint32_t parts_of(int H, int heads) { return ((uint32_t)H + heads - 1) / heads; }
-
-// A head row of a thread's pieces: copy from global memory (src: the row), and
-// read. From half to half: kPieces * kThreads * 16 bytes.
-template <typename T, int D, int kThreads>
-__device__ __forceinline__ void copy_row(uint32_t at, const T* src, int l, bool live) {
-    constexpr int kP = Raw8<T>::kPieces;
-#pragma unroll
-    for (int i = 0; i < 2 * kP; ++i)
-        copy16(at + i * kThreads * 16, src + i / kP * (D / 2) + i % kP * (D / 4) + Raw8<T>::kStep * l, live);
-}
-template <typename T, int kThreads>
-__device__ __forceinline__ Row read_row(uint32_t at) {
-    constexpr int kP = Raw8<T>::kPieces;
-    uint4 p[kP], q[kP];
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-        p[i] = ld_shared16(at + i * kThreads * 16);
-        q[i] = ld_shared16(at + (kP + i) * kThreads * 16);
-    }
-    return {Raw8<T>::get(p), Raw8<T>::get(q)};
-}
-
+// Units 0 .. q_units - 1 are the queries', the others the keys'.
 template <typename T, int D>
 __global__ void __launch_bounds__(Fwd<T, D>::kThreads, Fwd<T, D>::kCtas)
 norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __restrict__ q_out, T* __restrict__ k_out) {
     using S = Fwd<T, D>;
-    constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16;      // from row to row
+    constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16, kStage = S::kHeads * kRow;    // bytes from row to row, stage to stage
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t ring = sm100::smem_u32(smem) + threadIdx.x * 16;
     const int l = threadIdx.x % HeadRow<D>::kLanes;
@@ -90,21 +68,19 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
             const int H = is_k ? a.Hkv : a.Hq;
             const uint32_t parts = is_k ? parts_k : parts_q, w = is_k ? u - q_units : u, t = w / parts;
             const T* src = static_cast<const T*>(is_k ? a.k : a.q) + (long long)t * (is_k ? a.ld_k : a.ld_q);
-            const uint32_t at = ring + st * (S::kPieces * S::kThreads * 16);
 #pragma unroll
             for (int i = 0; i < S::kHeads; ++i) {
                 const int h = (int)(w - t * parts + i * parts);
-                copy_row<T, D, S::kThreads>(at + i * kRow, src + (h < H ? h : 0) * D, l, h < H);
+                copy_row<T, D, S::kThreads>(ring + st * kStage + i * kRow, src + (h < H ? h : 0) * D, l, h < H);
             }
         }
         copy_commit();
     };
 
-    uint32_t next = first;
+    uint32_t next = first, st = 0;
 #pragma unroll
     for (int s = 0; s < S::kStages; ++s, next += step) issue(next, s);
-    uint32_t st = 0;
-    // (units + step stays below 2^32: units is below 2^31)
+    // (no sum here passes 2^32: units is below 2^31)
     for (uint32_t base = blockIdx.x * S::kSlots, u = first; base < units; base += step, u += step) {
         const bool live = u < units, is_k = u >= q_units;
         const int H = is_k ? a.Hkv : a.Hq;
@@ -114,13 +90,11 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
         const Turn turn(load_angles<T, D>(a.table, max(pos, 0), l), load_weight<T, D>(weight, l));
         T* dst = (is_k ? k_out : q_out) + (long long)t * H * D;
         copy_wait<S::kStages - 1>();
-        const uint32_t at = ring + st * (S::kPieces * S::kThreads * 16);
 #pragma unroll
         for (int i = 0; i < S::kHeads; ++i) {
             const int h = (int)(w - t * parts + i * parts);
-            const Row x = read_row<T, S::kThreads>(at + i * kRow);
-            const float r = weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f;
-            Row y = turn(x, r);
+            const Row x = read_row<T, S::kThreads>(ring + st * kStage + i * kRow);
+            Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
             if (pos < 0) y = Row{};
             if (live && h < H) store_row<D>(dst + h * D, l, y);
         }

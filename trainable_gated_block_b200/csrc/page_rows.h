@@ -66,6 +66,11 @@ SAS_HD PageTile page_tile(const SeqNew& s, int i) {
 // Tiles that a sequence of at most max_new new tokens can touch.
 SAS_HD int max_tiles(int max_new) { return (max_new - 1 + kPageRows - 1) / kPageRows + 1; }
 
+// First of the tile indices of sequence n, whose rows start at token row lo, when
+// the tiles of all sequences are numbered by T / 64 + 2 N indices: it has at least
+// len / 64 + 2 of them, and its rows touch at most (len + 62) / 64 + 1 blocks.
+SAS_HD uint32_t seq_tile_base(int lo, int n) { return (uint32_t)(lo < 0 ? 0 : lo) / kPageRows + 2u * (uint32_t)n; }
+
 // Exponent of the least power of two s with amax <= 448 s, not under
 // kMinScaleExp. amax: finite and not negative, as its fp32 bits. 448 is
 // 1.75 * 2^8: a mantissa above 1.75 needs the next power.

@@ -209,13 +209,13 @@ sas_status append_impl(const char* fn, bool q8, const void* q, int64_t ld_q, con
     if ((r = check_rows(fn, "v", v, ld_v, Hkv, D, 2)) != SAS_OK) return r;
     if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kpool))
         return fail(SAS_ERR_INVALID_ARG, "%s: tensors not 16-byte aligned", fn);
-    if (T > ((1LL << 31) - 1) / Hq) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^31", fn);
+    if (T > ((1LL << 29) - 1) / Hq) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x query heads beyond 2^29", fn);
     if (max_new > (1 << 30)) return fail(SAS_ERR_UNSUPPORTED, "%s: max_new=%d (at most 2^30)", fn, max_new);
+    if ((T / 64 + 2LL * N + 1) > ((1LL << 29) - 1) / Hkv)
+        return fail(SAS_ERR_UNSUPPORTED, "%s: (T / 64 + 2 N) x Hkv beyond 2^29", fn);
     sas::AppendArgs a{q, ld_q, k, ld_k, v, ld_v, q_weight, k_weight, table, max_pos, cu_new, N, max_new, T, kv_len,
                       page_table, max_pages, num_pages, Hq, Hkv, eps, q_out, k_out, k_cache, v_cache, k_scale, v_scale,
                       kpool, nullptr};
-    if (sas::append_kv_ctas(a) > 1LL << 30)
-        return fail(SAS_ERR_UNSUPPORTED, "%s: N x blocks of max_new x Hkv beyond 2^29", fn);
     if (!(a.status = status_ptr())) return fail(SAS_ERR_CUDA, "%s: no CUDA device", fn);
     cudaError_t e = sas::launch_append(a, D, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, fn);
