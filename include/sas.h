@@ -457,7 +457,7 @@ sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void 
  * kpool      device fp32 [num_pages, Hkv, D] or NULL: pages whose last row this call
  *            writes get their mean key, as sas_pool_pages would write it.
  * A sequence whose lengths break these terms is flagged and skipped whole; a page id
- * outside 0 .. num_pages-1 is flagged and the rows for that page are skipped. Rows of
+ * outside 0 .. num_pages-1 is flagged and nothing is stored for it. Rows of
  * q_out and k_out that belong to no sequence, or to a skipped one, are left as they are.
  * Outputs must not overlap the inputs. D in {64, 128}, page_size 64, T * Hq and
  * (T / 64 + 2 N) * Hkv below 2^29.

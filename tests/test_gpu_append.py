@@ -447,3 +447,29 @@ def test_serving_loop_against_reference(q8):
             assert np.abs(R.f64(s)[n, :, :nh[n]] - sref[n, :, :nh[n]]).max(initial=0.0) <= 1e-5
         ro, rl = O.decode(q.cpu(), keys, vals, pt, kv, idx.cpu(), cnt.cpu(), gate.cpu(), 1 / math.sqrt(D))
         assert float(np.abs(R.f64(o) - ro).max()) <= 1e-2 and float(np.abs(R.f64(lse) - rl).max()) <= 1e-2
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond 4 GiB of the cache; only rows of the pages in use are looked at."""
+    D, Hq, Hkv, P = 128, 16, 8, 70000                            # 4.6 GB for each cache
+    table = sas.rope_table(200, D)
+    tok, dev = _tokens(130, Hq, Hkv, D, seed=31)
+    cu, kv = torch.tensor([0, 130], dtype=torch.int32), torch.tensor([130], dtype=torch.int32)
+    where = torch.tensor([[P - 1, 12345, P - 2]], dtype=torch.int32)
+    big, small = Cache.__new__(Cache), Cache(True, 3, Hkv, D, seed=32)
+    big.q8, big.P, big.Hkv, big.D = True, P, Hkv, D
+    big.k, big.v = (torch.empty((P, Hkv, 64, D), dtype=F8, device="cuda") for _ in range(2))
+    big.ks, big.vs = (torch.zeros((P, Hkv), device="cuda") for _ in range(2))
+    big.kpool = torch.zeros((P, Hkv, D), device="cuda")
+    for c, pt in ((big, where), (small, torch.tensor([[0, 1, 2]], dtype=torch.int32))):
+        c.append(*dev[:3], table, pt.cuda(), kv.cuda(), dev[3], cu_new=cu.cuda(), max_new=130)
+        one = [t[:1].contiguous() for t in dev[:3]]
+        c.append(*one, table, pt.cuda(), torch.tensor([131], dtype=torch.int32).cuda(), dev[3])
+    torch.cuda.synchronize()
+    sas.get_error_flag()
+    raw, at = torch.uint8, where[0].long().cuda()
+    for a, b in ((big.k, small.k), (big.v, small.v)):
+        a, b = a.view(raw)[at], b.view(raw)
+        assert torch.equal(a[:2], b[:2]) and torch.equal(a[2, :, :3], b[2, :, :3])
+    assert torch.equal(big.ks[at], small.ks) and torch.equal(big.vs[at], small.vs)
+    assert torch.equal(big.kpool[at[:2]], small.kpool[:2])
