@@ -392,6 +392,11 @@ def _expect_current(dev: int):
         raise ValueError("tensors must be on the current CUDA device")
 
 
+def _dense_like(t):
+    """An uninitialised contiguous tensor of t's shape, dtype and device (the cheapest way torch has)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _workspace(workspace, need: int, dev: int, like):
     """Address and bytes of the caller's workspace, or of a new one (third, to be kept until the launch)."""
     if workspace is None:
@@ -483,7 +488,7 @@ def qk_norm_rope(q, k, table, q_weight=None, k_weight=None, positions=None, eps:
     positions int32 of the token shape, or None: 0..S-1 in each sequence (3-D: one sequence).
     Returns contiguous q and k, as attn_fwd takes them."""
     code, args, (*_, dev) = _qk_args(q, k, table, q_weight, k_weight, positions, eps)
-    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
+    q_out, k_out = _dense_like(q), _dense_like(k)
     code = lib().sas_qk_norm_rope(code, *args, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(dev))
     if code:
         _check(code)
@@ -496,7 +501,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, q_weight=None, k_weight=None, 
     its inputs. Returns dq, dk (input dtype, contiguous) and the weights' gradients in fp32 (None without)."""
     code, args, (T, Hq, Hkv, D, dev) = _qk_args(q, k, table, q_weight, k_weight, positions, eps)
     up = (_expect("dq_out", dq_out, q.dtype, q.shape, dev), _expect("dk_out", dk_out, q.dtype, k.shape, dev))
-    dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
+    dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
     dwq = dwk = None
     if q_weight is not None:
         dwq, dwk = q.new_empty((2, D), dtype=_F32T).unbind()
@@ -534,8 +539,8 @@ def _append(q8, q, k, v, table, k_cache, v_cache, scales, page_table, kv_len, q_
     cu = None if cu_new is None else _expect("cu_new", cu_new, _I32, (N + 1,), dev)
     pool = None if kpool is None else _expect("kpool", kpool, _F32T, (P, Hkv, D), dev)
     _expect_current(dev)
-    q_out = q.new_empty((T, Hq, D))
-    k_out = k.new_empty((T, Hkv, D)) if with_k else None
+    q_out = _dense_like(q)
+    k_out = _dense_like(k) if with_k else None
     fn = lib().sas_append_paged_q8 if q8 else lib().sas_append_paged
     code = fn(q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, *w, tab, max_pos, cu, N, max_new, T, kv, pt,
               max_pages, P, Hq, Hkv, D, page_size, eps, q_out.data_ptr(), _addr(k_out), *store, pool, _raw_stream(dev))
