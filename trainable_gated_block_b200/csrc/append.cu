@@ -28,6 +28,7 @@
 
 #include <algorithm>
 
+#include "dependent.cuh"
 #include "head_row.cuh"
 #include "launch.h"
 #include "page_rows.h"
@@ -270,6 +271,7 @@ template <int D, bool kQ8>
 __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const AppendArgs a, uint32_t q_ctas) {
     constexpr int kSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
     __shared__ __align__(16) float red[kCtaWarps][kSumRows<D>][D];
+    after_previous();
     if (blockIdx.x < q_ctas)
         token_q<D>(a, blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes);
     else
@@ -537,6 +539,7 @@ append_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t i
     constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
     __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
     __shared__ float wmax[kThreads / 32];
+    after_previous();
     const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
     // both kinds in proportion, their sum to within one: where a CTA has a batch at least, all shares are >= 0
     const uint32_t c = blockIdx.x;
@@ -585,11 +588,12 @@ template <int D, bool kQ8>
 cudaError_t go(const AppendArgs& a, cudaStream_t st) {
     constexpr long long kSlots = kThreads / HeadRow<D>::kLanes;
     const long long items = append_items(a);
+    cudaError_t e;
     if (a.max_new == 1) {
         constexpr long long kTokenSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
         const long long q_ctas = a.q != nullptr ? (a.T * a.Hq + kTokenSlots - 1) / kTokenSlots : 0;
-        append_token_kernel<D, kQ8>
-            <<<(unsigned)(q_ctas + (items + kCtaWarps - 1) / kCtaWarps), kTokenThreads, 0, st>>>(a, (uint32_t)q_ctas);
+        e = launch_dependent(append_token_kernel<D, kQ8>, dim3((unsigned)(q_ctas + (items + kCtaWarps - 1) / kCtaWarps)),
+                             kTokenThreads, 0, st, a, (uint32_t)q_ctas);
     } else {
         int dev = 0, sms = 148;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -597,11 +601,11 @@ cudaError_t go(const AppendArgs& a, cudaStream_t st) {
             sms = 148;
         const long long q_units = a.q != nullptr ? a.T * parts_of(a.Hq, kHeads) : 0;
         const long long batches = (q_units + kSlots - 1) / kSlots, most = (long long)kCtas * sms;
-        append_kernel<D, kQ8><<<(unsigned)std::min(batches + items, most), kThreads, 0, st>>>(
-            a, (uint32_t)q_units, (uint32_t)batches, (uint32_t)items);
+        e = launch_dependent(append_kernel<D, kQ8>, dim3((unsigned)std::min(batches + items, most)), kThreads, 0, st, a,
+                             (uint32_t)q_units, (uint32_t)batches, (uint32_t)items);
     }
-    count_launches(1);
-    return cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 }  // namespace

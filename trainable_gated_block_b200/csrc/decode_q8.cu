@@ -38,6 +38,7 @@
 
 #include "byte_map.h"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "launch.h"
 #include "page_rows.h"
 #include "sm100.cuh"
@@ -202,8 +203,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the combine kernel may be scheduled now (it waits for this grid to finish)
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+    after_previous();
     const int range = warp * (int)gridDim.x + (int)blockIdx.x;
     if (range >= p.ranges) return;
 
@@ -466,9 +466,7 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
                          int G, int K, long long V, int ranges, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
     __shared__ float acc_s[kGroups][kD];
     __shared__ float2 ml_s[kGroups];
-    // launched as a programmatic dependent of decode_q8_kernel: its blocks may be
-    // resident before that grid ends; wait for its writes here
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const long long row = blockIdx.x;          // n * Hq + hq
     const int d = threadIdx.x % kD, grp = threadIdx.x / kD;
     const long long s0 = (row / Hq * Hkv + row % Hq / G) * (K + 1);
@@ -562,8 +560,8 @@ cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params&
     constexpr int kSmem = (int)Shape<kWarps, kDepth>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<kWarps, kDepth>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    decode_q8_kernel<kWarps, kDepth><<<lay.grid, kWarps * 32, kSmem, st>>>(map[0], map[1], map[2], map[3], p);
-    return cudaGetLastError();
+    return launch_dependent(decode_q8_kernel<kWarps, kDepth>, dim3(lay.grid), kWarps * 32, kSmem, st, map[0], map[1], map[2],
+                            map[3], p);
 }
 
 }  // namespace
@@ -609,23 +607,12 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     p.status = a.status;
     cudaError_t e = lay.many ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
     if (e != cudaSuccess) return e;
-    // programmatic dependent launch: the combine's blocks are placed while the decode grid drains
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.N * a.Hq));
-    cfg.blockDim = dim3(lay.nslot > 8 ? 4 * kD : kD);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const auto combine = lay.nslot > 8 ? decode_q8_combine_kernel<4> : decode_q8_combine_kernel<1>;
-    e = cudaLaunchKernelEx(&cfg, combine, (const float*)part_o, (const float*)part_ml, lay.nslot, a.Hq, a.Hkv, p.G, a.K,
-                           lay.V, lay.ranges, (__nv_bfloat16*)a.o, a.lse);
-    if (e != cudaSuccess) return e;
-    count_launches(2);
-    return cudaGetLastError();
+    count_launches(1);
+    e = launch_dependent(lay.nslot > 8 ? decode_q8_combine_kernel<4> : decode_q8_combine_kernel<1>, dim3((unsigned)(a.N * a.Hq)),
+                         lay.nslot > 8 ? 4 * kD : kD, 0, st, part_o, part_ml, lay.nslot, a.Hq, a.Hkv, p.G, a.K, lay.V,
+                         lay.ranges, (__nv_bfloat16*)a.o, a.lse);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 }  // namespace sas

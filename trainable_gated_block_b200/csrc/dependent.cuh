@@ -1,0 +1,37 @@
+// Launches that overlap the latency of a launch with the end of the kernel
+// in front of it in the stream (programmatic dependent launch). Every kernel
+// launched this way calls after_previous() before it touches memory, which
+// waits until that kernel has finished and its writes are visible: only the
+// placement of the CTAs comes early. In a stream of calls this saves one to two
+// microseconds a kernel (a ragged append 22.5 -> 20.2 us). kEarly = false is for
+// kernels that lose by it: early CTAs take the room that the previous kernel
+// leaves, so that not every SM gets its share of a persistent grid (norm +
+// rotation of 8k tokens, captured: 30.3 us, early 31.7).
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace sas {
+
+__device__ __forceinline__ void after_previous() {
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <bool kEarly = true, typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kEarly ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace sas

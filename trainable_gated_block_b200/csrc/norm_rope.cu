@@ -15,6 +15,7 @@
 // shared memory with cp.async.
 #include <algorithm>
 
+#include "dependent.cuh"
 #include "head_row.cuh"
 #include "launch.h"
 
@@ -57,6 +58,7 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
     using S = Fwd<T, D>;
     constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16, kStage = S::kHeads * kRow;    // bytes from row to row, stage to stage
     extern __shared__ __align__(16) uint8_t smem[];
+    after_previous();
     const uint32_t ring = sm100::smem_u32(smem) + threadIdx.x * 16;
     const int l = threadIdx.x % HeadRow<D>::kLanes;
     const uint32_t first = blockIdx.x * S::kSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * S::kSlots;
@@ -129,10 +131,9 @@ norm_rope_bwd_kernel(const NormRopeArgs a, const T* __restrict__ dq_out, const T
     using S = Bwd<T, D>;
     constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16;
     extern __shared__ __align__(16) uint8_t smem[];
+    after_previous();
     const uint32_t ring = sm100::smem_u32(smem) + threadIdx.x * 16;
     const int l = threadIdx.x % HeadRow<D>::kLanes, slot = threadIdx.x / HeadRow<D>::kLanes;
-    // the kernel that adds the CTAs' sums may be scheduled now (it waits for this grid to finish)
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
     const bool both = q_ctas == 0;
     for (int which = !both && blockIdx.x >= q_ctas; which < 2; ++which) {
         const uint32_t cta = !both && which ? blockIdx.x - q_ctas : blockIdx.x;
@@ -244,7 +245,7 @@ template <int D>
 __global__ void __launch_bounds__(1024)
 norm_rope_dw_kernel(const float* __restrict__ part, int q_ctas, int ctas, float* __restrict__ dwq, float* __restrict__ dwk) {
     __shared__ float acc[32][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const bool is_k = blockIdx.x >= D / 32;
     const int d = (int)(blockIdx.x % (D / 32)) * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
     const int lo = is_k ? q_ctas : 0, hi = is_k ? ctas : q_ctas;
@@ -279,10 +280,10 @@ cudaError_t fwd(const NormRopeArgs& a, void* q_out, void* k_out, cudaStream_t st
     const uint32_t uq = (uint32_t)a.T * parts_of(a.Hq, S::kHeads), n = uq + (uint32_t)a.T * parts_of(a.Hkv, S::kHeads);
     cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    norm_rope_kernel<T, D><<<grid_for(n, S::kSlots, S::kCtas), S::kThreads, S::kSmem, st>>>(
-        a, uq, n, static_cast<T*>(q_out), static_cast<T*>(k_out));
-    count_launches(1);
-    return cudaGetLastError();
+    e = launch_dependent<false>(norm_rope_kernel<T, D>, dim3(grid_for(n, S::kSlots, S::kCtas)), S::kThreads, S::kSmem, st, a, uq, n,
+                         static_cast<T*>(q_out), static_cast<T*>(k_out));
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 // CTAs of the gradient kernel. Up to kSplitWaves units for each resident row slot,
@@ -322,26 +323,15 @@ cudaError_t bwd(const NormRopeArgs& a, const void* dq_out, const void* dk_out, v
     float* part = static_cast<float*>(workspace);
     cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    norm_rope_bwd_kernel<T, D><<<grid.grid, S::kThreads, S::kSmem, st>>>(a, static_cast<const T*>(dq_out),
-                                                                        static_cast<const T*>(dk_out), static_cast<T*>(dq),
-                                                                        static_cast<T*>(dk), part, grid.q);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    count_launches(1);
-    if (dwq == nullptr) return cudaSuccess;
-    // programmatic dependent launch: placed while the gradient kernel drains
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (D / 32));
-    cfg.blockDim = dim3(1024);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel<D>, (const float*)part, (int)grid.q_parts, (int)grid.parts, dwq, dwk);
+    e = launch_dependent<false>(norm_rope_bwd_kernel<T, D>, dim3(grid.grid), S::kThreads, S::kSmem, st, a, static_cast<const T*>(dq_out),
+                         static_cast<const T*>(dk_out), static_cast<T*>(dq), static_cast<T*>(dk), part, grid.q);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    return cudaGetLastError();
+    if (dwq == nullptr) return cudaSuccess;
+    e = launch_dependent(norm_rope_dw_kernel<D>, dim3(2 * (D / 32)), 1024, 0, st, part, (int)grid.q_parts, (int)grid.parts, dwq,
+                         dwk);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 }  // namespace
