@@ -459,8 +459,8 @@ sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void 
  * A sequence whose lengths break these terms is flagged and skipped whole; a page id
  * outside 0 .. num_pages-1 is flagged and nothing is stored for it. Rows of
  * q_out and k_out that belong to no sequence, or to a skipped one, are left as they are.
- * Outputs must not overlap the inputs. D in {64, 128}, page_size 64, T * Hq and
- * (T / 64 + 2 N) * Hkv below 2^29.
+ * Outputs must not overlap the inputs. D in {64, 128}, page_size 64; T * Hq, T * Hkv
+ * and (T / 64 + 2 N) * Hkv below 2^29.
  */
 sas_status sas_append_paged(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
                             int64_t ld_v, const void *q_weight, const void *k_weight,

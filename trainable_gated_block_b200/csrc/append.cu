@@ -10,13 +10,14 @@
 // codes' subnormals. Norm, rotation and the division are in fp32; each value
 // is rounded once.
 //
-// One launch, of one of two kernels. Single tokens (max_new = 1) are bound by latency:
-// a row slot (the D / 16 lanes of a row, head_row.cuh) takes one query head, a
-// warp the new row of one (sequence, KV head) of K or of V. Prompts are bound by HBM:
-// persistent CTAs take (sequence, block, KV head) tiles of K and of V, so that new
-// rows are read and written once, their amax needs no second pass and no two
-// CTAs share a scale, and units of four query heads; each thread prefetches its
-// pieces of the next tile or unit with cp.async.
+// Single tokens (max_new = 1) are bound by latency: a row slot (the D / 16 lanes of
+// a row, head_row.cuh) takes one query head, a warp the new row of one (sequence, KV
+// head) of K or of V. Prompts are bound by HBM. Into bf16 pages, persistent CTAs take
+// units of four heads of one token of q, k or v, which share the token's angles.
+// Into 8-bit pages a scale needs all new rows of a page: there the units of k and v
+// are (sequence, block, KV head) tiles, so that new rows are read and written
+// once, their amax needs no second pass and no two CTAs share a scale. Each
+// thread prefetches its pieces of the next unit or tile with cp.async.
 //
 // Measured on one B200 (32/8 heads of 128): one token of one sequence 3.8 us (8.3
 // with a CTA's 64-row tile for it), of 64 sequences into 8-bit pages 7.4 us, two
@@ -137,6 +138,53 @@ __device__ __forceinline__ PageScale page_scale(int lo, float old, float m) {
 template <int D>
 constexpr int kSumRows = D == 128 ? 16 : 32;
 
+// The rare work on the rows of a page and head, by one warp: the codes of the
+// first `grown` rows times `ratio`, and with `pool` the mean of the page's 64 keys
+// (times their scale `unit`). Rows from `rows` on are not looked at. `red`: the
+// warp's [kSumRows][D] floats.
+template <int D, bool kQ8>
+__device__ __forceinline__ void page_rows(const AppendArgs& a, bool is_v, int page, int h, int rows, int grown, float ratio,
+                                          float unit, bool pool, float (*red)[D]) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
+    const long long head = (long long)page * a.Hkv + h, tile0 = head * kPageRows;
+#pragma unroll
+    for (int k = 0; k < kSumRows<D> / kPerWarp; ++k) {
+        Row sum{};
+#pragma unroll
+        for (int i = 0; i < kPageRows / kSumRows<D>; ++i) {
+            const int r = grp + kPerWarp * k + kSumRows<D> * i;
+            if (r >= rows) continue;
+            if (kQ8) {
+                uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (tile0 + r) * D + 8 * l;
+                uint2 c = *reinterpret_cast<const uint2*>(row), c2 = *reinterpret_cast<const uint2*>(row + D / 2);
+                if (r < grown) {
+                    *reinterpret_cast<uint2*>(row) = c = to_codes(from_codes(c), ratio);
+                    *reinterpret_cast<uint2*>(row + D / 2) = c2 = to_codes(from_codes(c2), ratio);
+                }
+                if (pool) {
+                    add(sum.a, from_codes(c));
+                    add(sum.b, from_codes(c2));
+                }
+            } else {
+                const bf16* row = static_cast<const bf16*>(a.k_cache) + (tile0 + r) * D + 8 * l;
+                const uint4 c[1] = {*reinterpret_cast<const uint4*>(row)}, c2[1] = {*reinterpret_cast<const uint4*>(row + D / 2)};
+                add(sum.a, Raw8<bf16>::get(c));
+                add(sum.b, Raw8<bf16>::get(c2));
+            }
+        }
+        if (pool) store_sum<D>(red[grp + kPerWarp * k], l, sum);
+    }
+    if (!pool) return;
+    __syncwarp();
+    for (int d = lane; d < D; d += 32) {
+        float m = 0.f;
+#pragma unroll 16
+        for (int i = 0; i < kSumRows<D>; ++i) m += red[i][d];
+        a.kpool[head * D + d] = m * unit * (1.f / kPageRows);
+    }
+}
+
 // ------------------------------------------------------------------ single tokens
 constexpr int kTokenThreads = 128;
 
@@ -164,7 +212,7 @@ __device__ __forceinline__ void token_q(const AppendArgs& a, uint32_t u) {
 // older rows. `red`: the warp's [kSumRows][D] floats.
 template <int D, bool kQ8>
 __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float (*red)[D]) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp;
+    constexpr int kLanes = HeadRow<D>::kLanes;
     const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
     if (u >= 2u * a.N * a.Hkv) return;
     const uint32_t n = u / (2u * a.Hkv), rest = u - n * 2u * a.Hkv;
@@ -197,7 +245,9 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float 
 
     Row x = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
     if (!is_v) {
-        x = norm_turn(x, w, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f, ang);
+        // the products in the order of the prompts' kernels: both store the same bits
+        const float r = weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f;
+        x = kQ8 ? norm_turn(x, w, r, ang) : Turn(ang, w)(x, r);
         if (k_out != nullptr && grp == 0) store_row<D>(k_out + (t.row * a.Hkv + h) * D, l, x);
     }
     if (!ok) return;
@@ -228,43 +278,7 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float 
     const bool grown = kQ8 && t.lo > 0 && !ps.keep, pool = !is_v && a.kpool != nullptr && t.lo == kPageRows - 1;
     if (!grown && !pool) return;
     __syncwarp();                                   // the new row is written
-    const float ratio = old * (1.f / ps.s);
-    const int rows = t.lo + pool;                   // with pool the new row is read back with the others
-#pragma unroll
-    for (int k = 0; k < kSumRows<D> / kPerWarp; ++k) {
-        Row sum{};
-#pragma unroll
-        for (int i = 0; i < kPageRows / kSumRows<D>; ++i) {
-            const int r = grp + kPerWarp * k + kSumRows<D> * i;
-            if (r >= rows) continue;
-            if (kQ8) {
-                uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (tile0 + r) * D + 8 * l;
-                uint2 c = *reinterpret_cast<const uint2*>(row), c2 = *reinterpret_cast<const uint2*>(row + D / 2);
-                if (grown && r < t.lo) {
-                    *reinterpret_cast<uint2*>(row) = c = to_codes(from_codes(c), ratio);
-                    *reinterpret_cast<uint2*>(row + D / 2) = c2 = to_codes(from_codes(c2), ratio);
-                }
-                if (pool) {
-                    add(sum.a, from_codes(c));
-                    add(sum.b, from_codes(c2));
-                }
-            } else {
-                const bf16* row = static_cast<const bf16*>(a.k_cache) + (tile0 + r) * D + 8 * l;
-                const uint4 c[1] = {*reinterpret_cast<const uint4*>(row)}, c2[1] = {*reinterpret_cast<const uint4*>(row + D / 2)};
-                add(sum.a, Raw8<bf16>::get(c));
-                add(sum.b, Raw8<bf16>::get(c2));
-            }
-        }
-        if (pool) store_sum<D>(red[grp + kPerWarp * k], l, sum);
-    }
-    if (!pool) return;
-    __syncwarp();
-    for (int d = lane; d < D; d += 32) {
-        float m = 0.f;
-#pragma unroll 16
-        for (int i = 0; i < kSumRows<D>; ++i) m += red[i][d];
-        a.kpool[((long long)page * a.Hkv + h) * D + d] = m * ps.s * (1.f / kPageRows);
-    }
+    page_rows<D, kQ8>(a, is_v, page, h, t.lo + pool, grown ? t.lo : 0, old * (1.f / ps.s), ps.s, pool, red);
 }
 
 template <int D, bool kQ8>
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Appen
         token_kv<D, kQ8>(a, (blockIdx.x - q_ctas) * kCtaWarps + threadIdx.x / 32, red[threadIdx.x / 32]);
 }
 
-// ------------------------------------------------------------------ prompts
+// ------------------------------------------------------------------ prompts into 8-bit pages
 constexpr int kThreads = 128;
 constexpr int kHeads = 4;                   // query heads of a unit
 constexpr int kCtas = 4;                    // resident CTAs of an SM
@@ -316,6 +330,20 @@ struct SeqAt {
         tile0 = seq_tile_base(__ldg(a.cu_new + at), at);
         tile1 = seq_tile_base(__ldg(a.cu_new + at + 1), at + 1);
     }
+    __device__ __forceinline__ bool holds(int t) const { return n >= 0 && !bad && t >= row0 && t - row0 < count; }
+    // Goes to the sequence of token row t; false for a row of none, or of one that is skipped.
+    __device__ __forceinline__ bool find(const AppendArgs& a, int t) {
+        if (holds(t)) return true;
+        int at = seq_of_row(a, t);
+        if (at < 0) return false;
+        load(a, at);
+        // a sequence that is skipped may overlap another, where cu_new decreases
+        for (at = 0; bad && at < a.N; ++at) {
+            load(a, at);
+            bad = !holds(t);
+        }
+        return holds(t);
+    }
 };
 __device__ __forceinline__ Work kv_work(const AppendArgs& a, SeqAt& s, uint32_t v, uint32_t rest) {
     Work k{};
@@ -346,14 +374,18 @@ __device__ __forceinline__ Work q_work(const AppendArgs& a, SeqAt& s, uint32_t b
     const uint32_t u = batch * (kThreads / HeadRow<D>::kLanes) + threadIdx.x / HeadRow<D>::kLanes;
     if (u < q_units) {
         const int t = (int)(u / parts_of(a.Hq, kHeads));
-        if (s.n < 0 || s.bad || t < s.row0 || t - s.row0 >= s.count) {
-            const int n = seq_of_row(a, t);
-            if (n >= 0) s.load(a, n);
-        }
         k.at = (int)u;
-        if (s.n >= 0 && !s.bad && t >= s.row0 && t - s.row0 < s.count) k.pos = s.first + (t - s.row0);
+        if (s.find(a, t)) k.pos = s.first + (t - s.row0);
     }
     return k;
+}
+
+// Flags every sequence that breaks the call's terms, also those that no token row
+// or tile index leads to (by the first CTA).
+__device__ __forceinline__ void flag_sequences(const AppendArgs& a) {
+    if (blockIdx.x != 0) return;
+    for (int n = threadIdx.x; n < a.N; n += kThreads)
+        if (load_seq(a, n).bad || __ldg(a.cu_new + n + 1) < __ldg(a.cu_new + n)) flag_status(a.status, kStatusBadData);
 }
 
 // Starts the copies of a piece of work into a stage.
@@ -402,7 +434,7 @@ __device__ __forceinline__ void store_unit(const AppendArgs& a, const Work& k, u
 }
 
 // `stage`: the CTA's whole stage of this tile, `at` this thread's pieces of it.
-template <int D, bool kQ8>
+template <int D>
 __device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, uint32_t at, uint8_t* stage, float* wmax) {
     constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
     const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, lo = k.lo(), hi = k.hi();
@@ -413,19 +445,8 @@ __device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, u
         if (k_out == nullptr) return;
     }
     const long long tile0 = page_ok ? ((long long)k.page * a.Hkv + k.h) * kPageRows : 0;      // row of the cache
-    float* scale = kQ8 ? (is_v ? a.v_scale : a.k_scale) + (page_ok ? (long long)k.page * a.Hkv + k.h : 0) : nullptr;
-    const float old = kQ8 && page_ok && lo > 0 ? *scale : 0.f;
-    if (!kQ8 && is_v) {             // values into bf16 pages: as they are
-        bf16* cache = static_cast<bf16*>(a.v_cache) + tile0 * D + 8 * l;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = slot + i * kSlots;
-            if (r < lo || r >= hi) continue;
-            *reinterpret_cast<uint4*>(cache + r * D) = ld_shared16(at + 2 * i * kThreads * 16);
-            *reinterpret_cast<uint4*>(cache + r * D + D / 2) = ld_shared16(at + (2 * i + 1) * kThreads * 16);
-        }
-        return;
-    }
+    float* scale = (is_v ? a.v_scale : a.k_scale) + (page_ok ? (long long)k.page * a.Hkv + k.h : 0);
+    const float old = page_ok && lo > 0 ? *scale : 0.f;
     const bf16* weight = static_cast<const bf16*>(a.k_weight);
     Row x[kRows];
 #pragma unroll
@@ -436,81 +457,64 @@ __device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, u
         const float rr = weight != nullptr ? row_rrms<D>(x[i], a.eps) : 1.f;
         x[i] = norm_turn(x[i], load_weight<bf16, D>(weight, l), rr,
                          load_angles<bf16, D>(a.table, k.pos * kPageRows + min(max(r, lo), hi - 1), l));
-        if (r < lo || r >= hi) {
+        if (r < lo || r >= hi)
             x[i] = Row{};               // not a new row: nothing of it counts
-        } else {
-            if (k_out != nullptr) store_row<D>(k_out + ((long long)(k.at + r - lo) * a.Hkv + k.h) * D, l, x[i]);
-            if (!kQ8 && page_ok) store_row<D>(static_cast<bf16*>(a.k_cache) + (tile0 + r) * D, l, x[i]);
-        }
+        else if (k_out != nullptr)
+            store_row<D>(k_out + ((long long)(k.at + r - lo) * a.Hkv + k.h) * D, l, x[i]);
     }
     if (!page_ok) return;
     const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows;
     Row sum{};
-    float unit = 1.f;               // what a pooled value is in
-
-    if constexpr (kQ8) {
-        uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D + 8 * l;
-        auto tile_max = [&] {
-            float m = 0.f;              // rows that are not new are zero here
+    uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D + 8 * l;
+    auto tile_max = [&] {
+        float m = 0.f;              // rows that are not new are zero here
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) m = row_max(x[i], m);
-            m = warp_max(m);
-            __syncthreads();            // the last maxima have been read
-            if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-            __syncthreads();            // (and every thread has read the old scale)
+        for (int i = 0; i < kRows; ++i) m = row_max(x[i], m);
+        m = warp_max(m);
+        __syncthreads();            // the last maxima have been read
+        if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
+        __syncthreads();            // (and every thread has read the old scale)
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
-            return m;
-        };
-        float m = tile_max();
-        if (m == INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                drop_infinities(x[i].a);
-                drop_infinities(x[i].b);
-            }
-            m = tile_max();
-        }
-        const PageScale ps = page_scale(lo, old, m);
-        if (!ps.ok) {
-            if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-            return;
-        }
-        const float inv = 1.f / ps.s, ratio = old * inv;
-        if (threadIdx.x == 0 && !ps.keep) *scale = ps.s;
-        unit = ps.s;
+        for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
+        return m;
+    };
+    float m = tile_max();
+    if (m == INFINITY) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int r = slot + i * kSlots;
-            if (r >= hi || (r < lo && ps.keep && !pool)) continue;
-            uint2* p = reinterpret_cast<uint2*>(cache + r * D);
-            uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2);
-            uint2 c, c2;
-            if (r >= lo) {
-                *p = c = to_codes(x[i].a, inv);
-                *p2 = c2 = to_codes(x[i].b, inv);
-            } else {
-                c = *p;
-                c2 = *p2;
-                if (!ps.keep) {
-                    *p = c = to_codes(from_codes(c), ratio);
-                    *p2 = c2 = to_codes(from_codes(c2), ratio);
-                }
-            }
-            if (pool) {
-                add(sum.a, from_codes(c));
-                add(sum.b, from_codes(c2));
+            drop_infinities(x[i].a);
+            drop_infinities(x[i].b);
+        }
+        m = tile_max();
+    }
+    const PageScale ps = page_scale(lo, old, m);
+    if (!ps.ok) {
+        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+        return;
+    }
+    const float inv = 1.f / ps.s, ratio = old * inv;
+    if (threadIdx.x == 0 && !ps.keep) *scale = ps.s;
+    #pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = slot + i * kSlots;
+        if (r >= hi || (r < lo && ps.keep && !pool)) continue;
+        uint2* p = reinterpret_cast<uint2*>(cache + r * D);
+        uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2);
+        uint2 c, c2;
+        if (r >= lo) {
+            *p = c = to_codes(x[i].a, inv);
+            *p2 = c2 = to_codes(x[i].b, inv);
+        } else {
+            c = *p;
+            c2 = *p2;
+            if (!ps.keep) {
+                *p = c = to_codes(from_codes(c), ratio);
+                *p2 = c2 = to_codes(from_codes(c2), ratio);
             }
         }
-    } else {
-        if (!pool) return;
-        const bf16* cache = static_cast<const bf16*>(a.k_cache) + tile0 * D + 8 * l;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {           // what this thread has stored, and older rows
-            const bf16* p = cache + (slot + i * kSlots) * D;
-            const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)}, v[1] = {*reinterpret_cast<const uint4*>(p + D / 2)};
-            add(sum.a, Raw8<bf16>::get(u));
-            add(sum.b, Raw8<bf16>::get(v));
+        if (pool) {
+            add(sum.a, from_codes(c));
+            add(sum.b, from_codes(c2));
         }
     }
     if (!pool) return;
@@ -524,7 +528,7 @@ __device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, u
         float m = 0.f;
 #pragma unroll 16
         for (int i = 0; i < kSlots; ++i) m += red[i][threadIdx.x];
-        a.kpool[((long long)k.page * a.Hkv + k.h) * D + threadIdx.x] = m * unit * (1.f / kPageRows);
+        a.kpool[((long long)k.page * a.Hkv + k.h) * D + threadIdx.x] = m * ps.s * (1.f / kPageRows);
     }
     __syncthreads();                // read before the stage's next copies
 }
@@ -533,9 +537,9 @@ __device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, u
 // runs of both (neighbouring tiles are the heads of one block, whose table rows
 // are then L1 hits; every gridDim-th tile instead takes 2 to 10% longer). It starts with a
 // batch of units, whose copies wait for no lookup.
-template <int D, bool kQ8>
+template <int D>
 __global__ void __launch_bounds__(kThreads, kCtas)
-append_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t items) {
+append_tiles_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t items) {
     constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
     __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
     __shared__ float wmax[kThreads / 32];
@@ -571,17 +575,115 @@ append_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t i
         issue<D>(a, next, ring + (st ^ 1) * kStageBytes);
         copy_wait<kStages - 1>();
         if (cur.tile())
-            store_tile<D, kQ8>(a, cur, ring + st * kStageBytes, ring_s + st * kStageBytes, wmax);
+            store_tile<D>(a, cur, ring + st * kStageBytes, ring_s + st * kStageBytes, wmax);
         else if (cur.is(Work::kUnit))
             store_unit<D>(a, cur, ring + st * kStageBytes);
         cur = next;
         st ^= 1;
     }
     copy_wait<0>();
-    // every sequence that breaks the call's terms, also those that no tile index leads to
-    if (blockIdx.x == 0)
-        for (int n = threadIdx.x; n < a.N; n += kThreads)
-            if (load_seq(a, n).bad || __ldg(a.cu_new + n + 1) < __ldg(a.cu_new + n)) flag_status(a.status, kStatusBadData);
+    flag_sequences(a);
+}
+
+// ------------------------------------------------------------------ prompts into bf16 pages
+// Units of four heads of one token: queries, keys, and values, which are copied as they are.
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const AppendArgs a, uint32_t q_parts, uint32_t units) {
+    constexpr int kSlots = kThreads / HeadRow<D>::kLanes, kRow = 2 * kThreads * 16;
+    __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
+    after_previous();
+    const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
+    const int l = threadIdx.x % HeadRow<D>::kLanes;
+    const uint32_t kv_parts = parts_of(a.Hkv, kHeads), per = q_parts + 2 * kv_parts;
+    const uint32_t first = blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * kSlots;
+
+    enum { kNone, kQ, kK, kV };
+    struct Unit {
+        int kind, t, part, pos, page;
+    };
+    SeqAt seq;
+    auto unit_at = [&](uint32_t u) {
+        Unit r{kNone, 0, 0, 0, 0};
+        if (u >= units) return r;
+        const uint32_t t = u / per, j = u - t * per;
+        if (!seq.find(a, (int)t)) return r;             // a row of no sequence, or of one that is skipped
+        r.t = (int)t;
+        r.pos = seq.first + (int)t - seq.row0;
+        r.kind = j < q_parts ? kQ : j < q_parts + kv_parts ? kK : kV;
+        r.part = (int)(j < q_parts ? j : j < q_parts + kv_parts ? j - q_parts : j - q_parts - kv_parts);
+        if (r.kind != kQ) r.page = __ldg(a.page_table + (long long)seq.n * a.max_pages + r.pos / kPageRows);    // in range by kv_len's check
+        return r;
+    };
+    auto issue = [&](const Unit& r, uint32_t at) {
+        if (r.kind != kNone) {
+            const bf16* src = r.kind == kQ   ? static_cast<const bf16*>(a.q) + r.t * a.ld_q
+                              : r.kind == kK ? static_cast<const bf16*>(a.k) + r.t * a.ld_k
+                                             : static_cast<const bf16*>(a.v) + r.t * a.ld_v;
+            const int H = r.kind == kQ ? a.Hq : a.Hkv, parts = (int)(r.kind == kQ ? q_parts : kv_parts);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int h = r.part + i * parts;
+                copy_row<bf16, D, kThreads>(at + i * kRow, src + (h < H ? h : 0) * D, l, h < H);
+            }
+        }
+        copy_commit();
+    };
+
+    Unit cur = unit_at(first);
+    issue(cur, ring);
+    uint32_t st = 0;
+    for (uint32_t base = blockIdx.x * kSlots, u = first; base < units; base += step, u += step) {
+        const Unit next = unit_at(u + step);
+        issue(next, ring + (st ^ 1) * kStageBytes);
+        const bool is_q = cur.kind == kQ, is_v = cur.kind == kV;
+        const bf16* weight = static_cast<const bf16*>(is_q ? a.q_weight : a.k_weight);
+        const Turn turn(load_angles<bf16, D>(a.table, cur.pos, l), load_weight<bf16, D>(weight, l));
+        const int H = is_q ? a.Hq : a.Hkv, parts = (int)(is_q ? q_parts : kv_parts);
+        const bool page_ok = cur.page >= 0 && cur.page < a.num_pages, live = cur.kind != kNone;
+        if (live && !page_ok && l == 0) flag_status(a.status, kStatusBadData);
+        // queries go to their row of q_out, keys and values to row pos % 64 of the page's tile of their head
+        bf16* dst = is_q ? static_cast<bf16*>(a.q_out) + (long long)cur.t * a.Hq * D
+                         : static_cast<bf16*>(is_v ? a.v_cache : a.k_cache) +
+                               ((long long)(page_ok ? cur.page : 0) * a.Hkv * kPageRows + cur.pos % kPageRows) * D;
+        const int stride = is_q ? D : kPageRows * D;
+        bf16* k_out = cur.kind == kK ? static_cast<bf16*>(a.k_out) : nullptr;
+        copy_wait<kStages - 1>();
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = cur.part + i * parts;
+            const uint32_t at = ring + st * kStageBytes + i * kRow;
+            const Row x = read_row<bf16, kThreads>(at);
+            const Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+            if (!live || h >= H) continue;
+            if (k_out != nullptr) store_row<D>(k_out + ((long long)cur.t * a.Hkv + h) * D, l, y);
+            if (!page_ok) continue;
+            bf16* p = dst + (long long)h * stride;
+            if (is_v) {
+                *reinterpret_cast<uint4*>(p + 8 * l) = ld_shared16(at);
+                *reinterpret_cast<uint4*>(p + D / 2 + 8 * l) = ld_shared16(at + kThreads * 16);
+            } else {
+                store_row<D>(p, l, y);
+            }
+        }
+        cur = next;
+        st ^= 1;
+    }
+    copy_wait<0>();
+    flag_sequences(a);
+}
+
+// The mean key of every page that the call has filled: a warp for each (block, KV head).
+template <int D>
+__global__ void __launch_bounds__(kThreads) pool_filled_kernel(const AppendArgs a, uint32_t items) {
+    constexpr int kCtaWarps = kThreads / 32;
+    __shared__ __align__(16) float red[kCtaWarps][kSumRows<D>][D];
+    after_previous();
+    const uint32_t it = blockIdx.x * kCtaWarps + threadIdx.x / 32;
+    if (it >= items) return;
+    SeqAt seq;
+    const Work k = kv_work(a, seq, it / a.Hkv, it % a.Hkv);
+    if (!k.is(Work::kK) || k.hi() != kPageRows || k.page < 0 || k.page >= a.num_pages) return;
+    page_rows<D, false>(a, false, k.page, k.h, kPageRows, 0, 1.f, 1.f, true, red[threadIdx.x / 32]);
 }
 
 template <int D, bool kQ8>
@@ -594,15 +696,28 @@ cudaError_t go(const AppendArgs& a, cudaStream_t st) {
         const long long q_ctas = a.q != nullptr ? (a.T * a.Hq + kTokenSlots - 1) / kTokenSlots : 0;
         e = launch_dependent(append_token_kernel<D, kQ8>, dim3((unsigned)(q_ctas + (items + kCtaWarps - 1) / kCtaWarps)),
                              kTokenThreads, 0, st, a, (uint32_t)q_ctas);
-    } else {
-        int dev = 0, sms = 148;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 148;
-        const long long q_units = a.q != nullptr ? a.T * parts_of(a.Hq, kHeads) : 0;
-        const long long batches = (q_units + kSlots - 1) / kSlots, most = (long long)kCtas * sms;
-        e = launch_dependent(append_kernel<D, kQ8>, dim3((unsigned)std::min(batches + items, most)), kThreads, 0, st, a,
+        if (e == cudaSuccess) count_launches(1);
+        return e;
+    }
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 148;
+    const long long q_parts = a.q != nullptr ? parts_of(a.Hq, kHeads) : 0, most = (long long)kCtas * sms;
+    if constexpr (kQ8) {
+        const long long q_units = a.T * q_parts, batches = (q_units + kSlots - 1) / kSlots;
+        e = launch_dependent(append_tiles_kernel<D>, dim3((unsigned)std::min(batches + items, most)), kThreads, 0, st, a,
                              (uint32_t)q_units, (uint32_t)batches, (uint32_t)items);
+    } else {
+        const long long units = a.T * (q_parts + 2 * parts_of(a.Hkv, kHeads));
+        e = launch_dependent(append_rows_kernel<D>, dim3((unsigned)std::min((units + kSlots - 1) / kSlots, most)), kThreads, 0,
+                             st, a, (uint32_t)q_parts, (uint32_t)units);
+        if (e == cudaSuccess && a.kpool != nullptr) {
+            count_launches(1);
+            constexpr int kCtaWarps = kThreads / 32;
+            const long long heads = items / 2;
+            e = launch_dependent(pool_filled_kernel<D>, dim3((unsigned)((heads + kCtaWarps - 1) / kCtaWarps)), kThreads, 0, st, a,
+                                 (uint32_t)heads);
+        }
     }
     if (e == cudaSuccess) count_launches(1);
     return e;

@@ -209,7 +209,8 @@ sas_status append_impl(const char* fn, bool q8, const void* q, int64_t ld_q, con
     if ((r = check_rows(fn, "v", v, ld_v, Hkv, D, 2)) != SAS_OK) return r;
     if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kpool))
         return fail(SAS_ERR_INVALID_ARG, "%s: tensors not 16-byte aligned", fn);
-    if (T > ((1LL << 29) - 1) / Hq) return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x query heads beyond 2^29", fn);
+    if (T > ((1LL << 29) - 1) / (Hq > Hkv ? Hq : Hkv))
+        return fail(SAS_ERR_UNSUPPORTED, "%s: token rows x heads beyond 2^29", fn);
     if (max_new > (1 << 30)) return fail(SAS_ERR_UNSUPPORTED, "%s: max_new=%d (at most 2^30)", fn, max_new);
     if ((T / 64 + 2LL * N + 1) > ((1LL << 29) - 1) / Hkv)
         return fail(SAS_ERR_UNSUPPORTED, "%s: (T / 64 + 2 N) x Hkv beyond 2^29", fn);
