@@ -15,15 +15,16 @@
 // head) of K or of V. Prompts are bound by HBM. Into bf16 pages, persistent CTAs take
 // units of four heads of one token of q, k or v, which share the token's angles.
 // Into 8-bit pages a scale needs all new rows of a page: there the units of k and v
-// are (sequence, block, KV head) tiles, so that new rows are read and written
-// once, their amax needs no second pass and no two CTAs share a scale. Each
-// thread prefetches its pieces of the next unit or tile with cp.async.
+// of one (sequence, block, pair of heads) go to one CTA, so that new rows are read
+// and written once, their amax needs no second pass and no two CTAs share a scale.
+// Each thread prefetches its pieces of the next unit with cp.async.
 //
-// Measured on one B200 (32/8 heads of 128): one token of one sequence 3.8 us (8.3
-// with a CTA's 64-row tile for it), of 64 sequences into 8-bit pages 7.4 us, two
-// of which fill a page, of 256 sequences 9.2 (22.5); prompts of 8k and 32k tokens
-// into bf16 pages 43 and 147 us (74 and 86% of the copy rate; 45 and 170 with one
-// CTA for each tile and four heads' loads in registers), 8k into 8-bit pages 43.8.
+// Measured on one B200 (32/8 heads of 128): one token of one sequence 3.4 us, of 64
+// sequences into 8-bit pages 6.9, two of which fill a page, of 256 sequences 9.2
+// (22.5 with a CTA for each row); prompts of 8k and 32k tokens into bf16 pages 36.8
+// and 127.5 us (86 and 100% of the copy rate; as 64-row tiles of one head 42.5 and
+// 147), into 8-bit pages 41.7 and 154 (70 and 76%): the blocks' barrier leaves the
+// latencies of one CTA's 16 warps in a row.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -245,9 +246,7 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float 
 
     Row x = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
     if (!is_v) {
-        // the products in the order of the prompts' kernels: both store the same bits
-        const float r = weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f;
-        x = kQ8 ? norm_turn(x, w, r, ang) : Turn(ang, w)(x, r);
+        x = Turn(ang, w)(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);     // as the prompts' kernels: the same bits
         if (k_out != nullptr && grp == 0) store_row<D>(k_out + (t.row * a.Hkv + h) * D, l, x);
     }
     if (!ok) return;
@@ -292,29 +291,12 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Appen
         token_kv<D, kQ8>(a, (blockIdx.x - q_ctas) * kCtaWarps + threadIdx.x / 32, red[threadIdx.x / 32]);
 }
 
-// ------------------------------------------------------------------ prompts into 8-bit pages
-constexpr int kThreads = 128;
-constexpr int kHeads = 4;                   // query heads of a unit
-constexpr int kCtas = 4;                    // resident CTAs of an SM
-constexpr int kStages = 2;                  // pieces of work in flight
-constexpr int kStageBytes = 2 * kHeads * kThreads * 16;    // a thread's pieces of a unit, or of its rows of a tile
+// ------------------------------------------------------------------ prompts
+constexpr int kHeads = 4;                   // heads of a unit, which is of one token
+constexpr int kStages = 2;                  // units in flight
 
-// A piece of work of a CTA: a (sequence, block, KV head) tile of K or of V with new
-// rows, or a query unit for each of its row slots, in few registers: one waits while
-// the other is worked on.
-struct Work {
-    enum : uint32_t { kNone, kUnit, kK, kV };
-    uint32_t kind;          // bits 0-1; of a tile: rows lo (bits 8-15) to hi (bits 16-23)
-    int at;                 // a unit: its number; a tile: the token row of its first new row
-    int pos;                // a unit: its position (append_pos); a tile: its block
-    int h, page;            // a tile's KV head and page
-    __device__ __forceinline__ bool is(uint32_t k) const { return (kind & 3) == k; }
-    __device__ __forceinline__ bool tile() const { return kind & 2; }
-    __device__ __forceinline__ int lo() const { return kind >> 8 & 255; }
-    __device__ __forceinline__ int hi() const { return kind >> 16; }
-};
-// The sequence that a thread's last piece of work belonged to. The next one mostly
-// belongs to it too, and then no load stands in front of its copies.
+// The sequence of a thread's last unit. The next one mostly belongs to it too, and
+// then no load stands in front of its copies.
 struct SeqAt {
     int n = -1;                 // -1: none yet
     int row0 = 0, count = 0, first = 0;
@@ -344,249 +326,61 @@ struct SeqAt {
         }
         return holds(t);
     }
-};
-__device__ __forceinline__ Work kv_work(const AppendArgs& a, SeqAt& s, uint32_t v, uint32_t rest) {
-    Work k{};
-    const bool is_v = rest >= (uint32_t)a.Hkv;
-    if (s.n < 0 || v < s.tile0 || v >= s.tile1) {       // the last n with its tile base <= v
-        int lo = 0, hi = a.N;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (seq_tile_base(__ldg(a.cu_new + mid), mid) <= v) lo = mid; else hi = mid;
+    // Goes to the sequence of tile index v, and says which of its new rows the tile has (none: empty).
+    __device__ __forceinline__ PageTile find_tile(const AppendArgs& a, uint32_t v) {
+        if (n < 0 || v < tile0 || v >= tile1) {         // the last n with its tile base <= v
+            int lo = 0, hi = a.N;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (seq_tile_base(__ldg(a.cu_new + mid), mid) <= v) lo = mid; else hi = mid;
+            }
+            load(a, lo);
         }
-        s.load(a, lo);
+        if (bad || v < tile0 || v - tile0 >= (uint32_t)max_tiles(a.max_new)) return PageTile{0, 0, 0, 0};
+        return page_tile(SeqNew{row0, first, count, false}, (int)(v - tile0));
     }
-    if (s.bad || v < s.tile0 || v - s.tile0 >= (uint32_t)max_tiles(a.max_new)) return k;
-    const PageTile t = page_tile(SeqNew{s.row0, s.first, s.count, false}, (int)(v - s.tile0));
-    if (t.hi <= t.lo) return k;
-    k.kind = (is_v ? Work::kV : Work::kK) | (uint32_t)t.lo << 8 | (uint32_t)t.hi << 16;
-    k.at = (int)t.row;
-    k.pos = t.block;
-    k.h = (int)(is_v ? rest - a.Hkv : rest);
-    k.page = __ldg(a.page_table + (long long)s.n * a.max_pages + t.block);     // block < max_pages by kv_len's check
-    return k;
-}
-template <int D>
-__device__ __forceinline__ Work q_work(const AppendArgs& a, SeqAt& s, uint32_t batch, uint32_t q_units) {
-    Work k{};
-    k.kind = Work::kUnit;
-    k.pos = -2;
-    const uint32_t u = batch * (kThreads / HeadRow<D>::kLanes) + threadIdx.x / HeadRow<D>::kLanes;
-    if (u < q_units) {
-        const int t = (int)(u / parts_of(a.Hq, kHeads));
-        k.at = (int)u;
-        if (s.find(a, t)) k.pos = s.first + (t - s.row0);
+    __device__ __forceinline__ int page(const AppendArgs& a, int block) const {     // block < max_pages by kv_len's check
+        return __ldg(a.page_table + (long long)n * a.max_pages + block);
     }
-    return k;
-}
-
+};
 // Flags every sequence that breaks the call's terms, also those that no token row
 // or tile index leads to (by the first CTA).
 __device__ __forceinline__ void flag_sequences(const AppendArgs& a) {
     if (blockIdx.x != 0) return;
-    for (int n = threadIdx.x; n < a.N; n += kThreads)
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x)
         if (load_seq(a, n).bad || __ldg(a.cu_new + n + 1) < __ldg(a.cu_new + n)) flag_status(a.status, kStatusBadData);
 }
 
-// Starts the copies of a piece of work into a stage.
-template <int D>
-__device__ __forceinline__ void issue(const AppendArgs& a, const Work& k, uint32_t at) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
-    const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-    if (k.tile()) {
-        const bool is_v = k.is(Work::kV);
-        const bf16* src = (is_v ? static_cast<const bf16*>(a.v) : static_cast<const bf16*>(a.k)) + k.h * D;
-        const long long ld = is_v ? a.ld_v : a.ld_k;
-        const int lo = k.lo(), hi = k.hi();
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = slot + i * kSlots;        // rows that are not new: zeroes, copied from nowhere
-            copy_row<bf16, D, kThreads>(at + 2 * i * kThreads * 16, src + (k.at + min(max(r, lo), hi - 1) - lo) * ld, l,
-                                        r >= lo && r < hi);
-        }
-    } else if (k.is(Work::kUnit) && k.pos > -2) {
-        const uint32_t parts = parts_of(a.Hq, kHeads), t = k.at / parts;
-        const bf16* src = static_cast<const bf16*>(a.q) + (long long)t * a.ld_q;
+enum UnitKind { kNone, kQ, kK, kV };
+// A row slot's unit: heads part, part + parts, ... of a token's row of q, k or v.
+struct Unit {
+    int kind, t, part, pos, page;
+};
+// Starts the copies of a unit (row pieces of kThreads threads each) into a stage.
+template <int D, int kThreads, int kKvHeads>
+__device__ __forceinline__ void issue(const AppendArgs& a, const Unit& r, uint32_t at) {
+    const int l = threadIdx.x % HeadRow<D>::kLanes;
+    if (r.kind != kNone) {
+        const bf16* src = r.kind == kQ   ? static_cast<const bf16*>(a.q) + r.t * a.ld_q
+                          : r.kind == kK ? static_cast<const bf16*>(a.k) + r.t * a.ld_k
+                                         : static_cast<const bf16*>(a.v) + r.t * a.ld_v;
+        const int H = r.kind == kQ ? a.Hq : a.Hkv, heads = r.kind == kQ ? kHeads : kKvHeads, parts = (int)parts_of(H, heads);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            const int h = (int)(k.at - t * parts + i * parts);
-            copy_row<bf16, D, kThreads>(at + 2 * i * kThreads * 16, src + (h < a.Hq ? h : 0) * D, l, h < a.Hq);
+            if (i >= heads) break;
+            const int h = r.part + i * parts;
+            copy_row<bf16, D, kThreads>(at + 2 * i * kThreads * 16, src + (h < H ? h : 0) * D, l, h < H);
         }
     }
     copy_commit();
 }
 
-template <int D>
-__device__ __forceinline__ void store_unit(const AppendArgs& a, const Work& k, uint32_t at) {
-    const int l = threadIdx.x % HeadRow<D>::kLanes;
-    const bf16* weight = static_cast<const bf16*>(a.q_weight);
-    const uint32_t parts = parts_of(a.Hq, kHeads), t = k.at / parts;
-    const Turn turn(load_angles<bf16, D>(a.table, max(k.pos, 0), l), load_weight<bf16, D>(weight, l));
-    bf16* dst = static_cast<bf16*>(a.q_out) + (long long)t * a.Hq * D;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = (int)(k.at - t * parts + i * parts);
-        const Row x = read_row<bf16, kThreads>(at + 2 * i * kThreads * 16);
-        Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
-        if (k.pos < 0) y = Row{};
-        if (k.pos > -2 && h < a.Hq) store_row<D>(dst + h * D, l, y);
-    }
-}
-
-// `stage`: the CTA's whole stage of this tile, `at` this thread's pieces of it.
-template <int D>
-__device__ __forceinline__ void store_tile(const AppendArgs& a, const Work& k, uint32_t at, uint8_t* stage, float* wmax) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kSlots = kThreads / kLanes, kRows = kPageRows / kSlots;
-    const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, lo = k.lo(), hi = k.hi();
-    const bool is_v = k.is(Work::kV), page_ok = k.page >= 0 && k.page < a.num_pages;
-    bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
-    if (!page_ok) {
-        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-        if (k_out == nullptr) return;
-    }
-    const long long tile0 = page_ok ? ((long long)k.page * a.Hkv + k.h) * kPageRows : 0;      // row of the cache
-    float* scale = (is_v ? a.v_scale : a.k_scale) + (page_ok ? (long long)k.page * a.Hkv + k.h : 0);
-    const float old = page_ok && lo > 0 ? *scale : 0.f;
-    const bf16* weight = static_cast<const bf16*>(a.k_weight);
-    Row x[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = slot + i * kSlots;
-        x[i] = read_row<bf16, kThreads>(at + 2 * i * kThreads * 16);
-        if (is_v) continue;
-        const float rr = weight != nullptr ? row_rrms<D>(x[i], a.eps) : 1.f;
-        x[i] = norm_turn(x[i], load_weight<bf16, D>(weight, l), rr,
-                         load_angles<bf16, D>(a.table, k.pos * kPageRows + min(max(r, lo), hi - 1), l));
-        if (r < lo || r >= hi)
-            x[i] = Row{};               // not a new row: nothing of it counts
-        else if (k_out != nullptr)
-            store_row<D>(k_out + ((long long)(k.at + r - lo) * a.Hkv + k.h) * D, l, x[i]);
-    }
-    if (!page_ok) return;
-    const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows;
-    Row sum{};
-    uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile0 * D + 8 * l;
-    auto tile_max = [&] {
-        float m = 0.f;              // rows that are not new are zero here
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) m = row_max(x[i], m);
-        m = warp_max(m);
-        __syncthreads();            // the last maxima have been read
-        if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
-        __syncthreads();            // (and every thread has read the old scale)
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, wmax[i]);
-        return m;
-    };
-    float m = tile_max();
-    if (m == INFINITY) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            drop_infinities(x[i].a);
-            drop_infinities(x[i].b);
-        }
-        m = tile_max();
-    }
-    const PageScale ps = page_scale(lo, old, m);
-    if (!ps.ok) {
-        if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-        return;
-    }
-    const float inv = 1.f / ps.s, ratio = old * inv;
-    if (threadIdx.x == 0 && !ps.keep) *scale = ps.s;
-    #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = slot + i * kSlots;
-        if (r >= hi || (r < lo && ps.keep && !pool)) continue;
-        uint2* p = reinterpret_cast<uint2*>(cache + r * D);
-        uint2* p2 = reinterpret_cast<uint2*>(cache + r * D + D / 2);
-        uint2 c, c2;
-        if (r >= lo) {
-            *p = c = to_codes(x[i].a, inv);
-            *p2 = c2 = to_codes(x[i].b, inv);
-        } else {
-            c = *p;
-            c2 = *p2;
-            if (!ps.keep) {
-                *p = c = to_codes(from_codes(c), ratio);
-                *p2 = c2 = to_codes(from_codes(c2), ratio);
-            }
-        }
-        if (pool) {
-            add(sum.a, from_codes(c));
-            add(sum.b, from_codes(c2));
-        }
-    }
-    if (!pool) return;
-    // the filled page's mean key: the slots' sums in slot order, where the rows were
-    static_assert(kSlots == kSumRows<D> && kSlots * D * 4 <= kStageBytes, "sums of a tile");
-    float(*red)[D] = reinterpret_cast<float(*)[D]>(stage);
-    __syncthreads();                // every thread has its rows
-    store_sum<D>(red[slot], l, sum);
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float m = 0.f;
-#pragma unroll 16
-        for (int i = 0; i < kSlots; ++i) m += red[i][threadIdx.x];
-        a.kpool[((long long)k.page * a.Hkv + k.h) * D + threadIdx.x] = m * ps.s * (1.f / kPageRows);
-    }
-    __syncthreads();                // read before the stage's next copies
-}
-
-// A CTA's share: batches of query units (kSlots units each) and tiles, contiguous
-// runs of both (neighbouring tiles are the heads of one block, whose table rows
-// are then L1 hits; every gridDim-th tile instead takes 2 to 10% longer). It starts with a
-// batch of units, whose copies wait for no lookup.
-template <int D>
-__global__ void __launch_bounds__(kThreads, kCtas)
-append_tiles_kernel(const AppendArgs a, uint32_t q_units, uint32_t batches, uint32_t items) {
-    constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
-    __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
-    __shared__ float wmax[kThreads / 32];
-    after_previous();
-    const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
-    // both kinds in proportion, their sum to within one: where a CTA has a batch at least, all shares are >= 0
-    const uint32_t c = blockIdx.x;
-    auto share = [&](unsigned long long n, uint32_t c) { return (uint32_t)(n * c / gridDim.x); };
-    const unsigned long long all = (unsigned long long)batches + items;
-    uint32_t kv0 = share(items, c), kv1 = share(items, c + 1), q0 = share(all, c) - kv0, q1 = share(all, c + 1) - kv1;
-    if (batches < gridDim.x) {          // few batches: one list, the batches first
-        const uint32_t b0 = share(all, c), b1 = share(all, c + 1);
-        q0 = min(b0, batches), q1 = min(b1, batches);
-        kv0 = max(b0, batches) - batches, kv1 = max(b1, batches) - batches;
-    }
-    const uint32_t lead = q1 > q0 ? 1 : 0, tiles = kv1 - kv0, count = q1 - q0 + tiles;
-    static_assert(kStages == 2, "one piece of work waits");
-    SeqAt seq;
-    uint32_t v = kv0 / (2u * a.Hkv), rest = kv0 - v * 2u * a.Hkv;       // the next tile: its index, and head of K or of V
-    auto work_at = [&](uint32_t j) {
-        if (j >= lead && j < lead + tiles) {
-            const Work k = kv_work(a, seq, v, rest);
-            if (++rest == 2u * a.Hkv) rest = 0, ++v;
-            return k;
-        }
-        return q_work<D>(a, seq, q0 + (j < lead ? j : j - tiles), j < count ? q_units : 0);
-    };
-    Work cur = work_at(0);
-    issue<D>(a, cur, ring);
-    uint32_t st = 0;
-    for (uint32_t j = 0; j < count; ++j) {
-        const Work next = work_at(j + 1);
-        issue<D>(a, next, ring + (st ^ 1) * kStageBytes);
-        copy_wait<kStages - 1>();
-        if (cur.tile())
-            store_tile<D>(a, cur, ring + st * kStageBytes, ring_s + st * kStageBytes, wmax);
-        else if (cur.is(Work::kUnit))
-            store_unit<D>(a, cur, ring + st * kStageBytes);
-        cur = next;
-        st ^= 1;
-    }
-    copy_wait<0>();
-    flag_sequences(a);
-}
-
 // ------------------------------------------------------------------ prompts into bf16 pages
-// Units of four heads of one token: queries, keys, and values, which are copied as they are.
+constexpr int kThreads = 128;
+constexpr int kCtas = 4;                    // resident CTAs of an SM
+constexpr int kStageBytes = 2 * kHeads * kThreads * 16;
+
+// Units of queries, keys, and values, which are copied as they are.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const AppendArgs a, uint32_t q_parts, uint32_t units) {
     constexpr int kSlots = kThreads / HeadRow<D>::kLanes, kRow = 2 * kThreads * 16;
@@ -597,10 +391,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
     const uint32_t kv_parts = parts_of(a.Hkv, kHeads), per = q_parts + 2 * kv_parts;
     const uint32_t first = blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * kSlots;
 
-    enum { kNone, kQ, kK, kV };
-    struct Unit {
-        int kind, t, part, pos, page;
-    };
     SeqAt seq;
     auto unit_at = [&](uint32_t u) {
         Unit r{kNone, 0, 0, 0, 0};
@@ -611,30 +401,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
         r.pos = seq.first + (int)t - seq.row0;
         r.kind = j < q_parts ? kQ : j < q_parts + kv_parts ? kK : kV;
         r.part = (int)(j < q_parts ? j : j < q_parts + kv_parts ? j - q_parts : j - q_parts - kv_parts);
-        if (r.kind != kQ) r.page = __ldg(a.page_table + (long long)seq.n * a.max_pages + r.pos / kPageRows);    // in range by kv_len's check
+        if (r.kind != kQ) r.page = seq.page(a, r.pos / kPageRows);
         return r;
     };
-    auto issue = [&](const Unit& r, uint32_t at) {
-        if (r.kind != kNone) {
-            const bf16* src = r.kind == kQ   ? static_cast<const bf16*>(a.q) + r.t * a.ld_q
-                              : r.kind == kK ? static_cast<const bf16*>(a.k) + r.t * a.ld_k
-                                             : static_cast<const bf16*>(a.v) + r.t * a.ld_v;
-            const int H = r.kind == kQ ? a.Hq : a.Hkv, parts = (int)(r.kind == kQ ? q_parts : kv_parts);
-#pragma unroll
-            for (int i = 0; i < kHeads; ++i) {
-                const int h = r.part + i * parts;
-                copy_row<bf16, D, kThreads>(at + i * kRow, src + (h < H ? h : 0) * D, l, h < H);
-            }
-        }
-        copy_commit();
-    };
-
     Unit cur = unit_at(first);
-    issue(cur, ring);
+    issue<D, kThreads, kHeads>(a, cur, ring);
     uint32_t st = 0;
     for (uint32_t base = blockIdx.x * kSlots, u = first; base < units; base += step, u += step) {
         const Unit next = unit_at(u + step);
-        issue(next, ring + (st ^ 1) * kStageBytes);
+        issue<D, kThreads, kHeads>(a, next, ring + (st ^ 1) * kStageBytes);
         const bool is_q = cur.kind == kQ, is_v = cur.kind == kV;
         const bf16* weight = static_cast<const bf16*>(is_q ? a.q_weight : a.k_weight);
         const Turn turn(load_angles<bf16, D>(a.table, cur.pos, l), load_weight<bf16, D>(weight, l));
@@ -681,40 +456,243 @@ __global__ void __launch_bounds__(kThreads) pool_filled_kernel(const AppendArgs 
     const uint32_t it = blockIdx.x * kCtaWarps + threadIdx.x / 32;
     if (it >= items) return;
     SeqAt seq;
-    const Work k = kv_work(a, seq, it / a.Hkv, it % a.Hkv);
-    if (!k.is(Work::kK) || k.hi() != kPageRows || k.page < 0 || k.page >= a.num_pages) return;
-    page_rows<D, false>(a, false, k.page, k.h, kPageRows, 0, 1.f, 1.f, true, red[threadIdx.x / 32]);
+    const PageTile t = seq.find_tile(a, it / a.Hkv);
+    if (t.hi != kPageRows || t.hi <= t.lo) return;
+    const int page = seq.page(a, t.block);
+    if (page < 0 || page >= a.num_pages) return;
+    page_rows<D, false>(a, false, page, (int)(it % a.Hkv), kPageRows, 0, 1.f, 1.f, true, red[threadIdx.x / 32]);
+}
+
+// ------------------------------------------------------------------ prompts into 8-bit pages
+// A CTA with a row slot for each row of a page. Its work: 64 units of queries, or of
+// keys (values) those of the new rows of one (sequence, block, group of heads), whose
+// scales the CTA finds in shared memory while the values wait in registers.
+template <int D>
+struct Blocks {
+    static constexpr int kThreads = kPageRows * HeadRow<D>::kLanes, kCtas = 512 / kThreads;     // CTAs of an SM
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kKvHeads = 2;       // heads of a unit of keys or values (four would not fit the registers)
+    static constexpr int kStageBytes = 2 * kHeads * kThreads * 16;
+    static constexpr int kSmem = kStages * kStageBytes;
+};
+template <int D>
+__global__ void __launch_bounds__(Blocks<D>::kThreads, Blocks<D>::kCtas)
+append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, uint32_t works) {
+    using B = Blocks<D>;
+    extern __shared__ __align__(16) uint8_t ring_s[];
+    __shared__ float wmax[2][B::kKvHeads][B::kWarps];
+    after_previous();
+    const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
+    const int l = threadIdx.x % HeadRow<D>::kLanes, slot = threadIdx.x / HeadRow<D>::kLanes;
+    const int q_parts = (int)parts_of(a.Hq, kHeads), kv_parts = (int)parts_of(a.Hkv, B::kKvHeads);
+
+    // the unit, and of a block of keys or values its rows lo .. hi - 1 that are new (all slots: `rows`, 0: none)
+    struct Work {
+        Unit u;
+        int rows;
+        __device__ __forceinline__ int lo() const { return rows & 255; }
+        __device__ __forceinline__ int hi() const { return rows >> 8; }
+    };
+    SeqAt seq;
+    auto work_at = [&](uint32_t w) {
+        Work k{{kNone, 0, 0, 0, 0}, 0};
+        if (w >= works) return k;
+        if (w >= kv_works) {
+            const uint32_t u = (w - kv_works) * kPageRows + slot, t = u / q_parts;
+            if (u >= q_units || !seq.find(a, (int)t)) return k;
+            k.u = {kQ, (int)t, (int)(u - t * q_parts), seq.first + (int)t - seq.row0, 0};
+            return k;
+        }
+        const uint32_t v = w / (2u * kv_parts), rest = w - v * 2u * kv_parts;
+        const PageTile t = seq.find_tile(a, v);
+        if (t.hi <= t.lo) return k;
+        k.rows = t.lo | t.hi << 8;
+        const bool is_v = rest >= (uint32_t)kv_parts;
+        k.u.part = (int)(is_v ? rest - kv_parts : rest);
+        k.u.pos = t.block * kPageRows + slot;
+        k.u.page = seq.page(a, t.block);
+        k.u.t = (int)t.row + slot - t.lo;
+        k.u.kind = is_v ? kV : kK;
+        return k;
+    };
+    // copies of the rows that there are: the others' slots have nothing to copy
+    auto issue_work = [&](const Work& k, uint32_t at) {
+        Unit u = k.u;
+        if (k.rows != 0 && (slot < k.lo() || slot >= k.hi())) u.kind = kNone;
+        issue<D, B::kThreads, B::kKvHeads>(a, u, at);
+    };
+    constexpr int kRow = 2 * B::kThreads * 16;
+
+    Work cur = work_at(blockIdx.x);
+    issue_work(cur, ring);
+    uint32_t st = 0, buf = 0;
+    for (uint32_t w = blockIdx.x; w < works; w += gridDim.x) {
+        const Work next = work_at(w + gridDim.x);
+        issue_work(next, ring + (st ^ 1) * B::kStageBytes);
+        copy_wait<kStages - 1>();
+        const uint32_t at = ring + st * B::kStageBytes;
+        st ^= 1;
+        const Unit& u = cur.u;
+        if (cur.rows == 0) {
+            // queries
+            const bf16* weight = static_cast<const bf16*>(a.q_weight);
+            const Turn turn(load_angles<bf16, D>(a.table, u.pos, l), load_weight<bf16, D>(weight, l));
+            bf16* dst = static_cast<bf16*>(a.q_out) + (long long)u.t * a.Hq * D;
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int h = u.part + i * q_parts;
+                const Row x = read_row<bf16, B::kThreads>(at + i * kRow);
+                const Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+                if (u.kind == kQ && h < a.Hq) store_row<D>(dst + h * D, l, y);
+            }
+            cur = next;
+            continue;
+        }
+        // keys or values (uniform over the CTA up to the slot's row)
+        const int lo = cur.lo(), hi = cur.hi();
+        const bool is_v = u.kind == kV, fresh = slot >= lo && slot < hi, page_ok = u.page >= 0 && u.page < a.num_pages;
+        if (!page_ok && threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+        bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
+        const long long head0 = (long long)(page_ok ? u.page : 0) * a.Hkv;
+        float* scale = (is_v ? a.v_scale : a.k_scale) + head0;
+        float old[B::kKvHeads];
+#pragma unroll
+        for (int i = 0; i < B::kKvHeads; ++i) {
+            const int h = u.part + i * kv_parts;
+            old[i] = page_ok && lo > 0 && h < a.Hkv ? scale[h] : 0.f;
+        }
+        Row y[B::kKvHeads];
+        if (is_v) {
+#pragma unroll
+            for (int i = 0; i < B::kKvHeads; ++i) y[i] = read_row<bf16, B::kThreads>(at + i * kRow);
+        } else {
+            const bf16* weight = static_cast<const bf16*>(a.k_weight);
+            const int pos = min(max(u.pos, u.pos - slot + lo), u.pos - slot + hi - 1);
+            const Turn turn(load_angles<bf16, D>(a.table, pos, l), load_weight<bf16, D>(weight, l));
+#pragma unroll
+            for (int i = 0; i < B::kKvHeads; ++i) {
+                const int h = u.part + i * kv_parts;
+                const Row x = read_row<bf16, B::kThreads>(at + i * kRow);
+                y[i] = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+                if (k_out != nullptr && fresh && h < a.Hkv) store_row<D>(k_out + ((long long)u.t * a.Hkv + h) * D, l, y[i]);
+            }
+        }
+        float m[B::kKvHeads];
+        auto block_max = [&] {
+#pragma unroll
+            for (int i = 0; i < B::kKvHeads; ++i) {
+                const float r = warp_max(fresh ? row_max(y[i], 0.f) : 0.f);
+                if ((threadIdx.x & 31) == 0) wmax[buf][i][threadIdx.x >> 5] = r;
+            }
+            __syncthreads();        // (and every thread has read the old scales, and its rows of this stage)
+#pragma unroll
+            for (int i = 0; i < B::kKvHeads; ++i) {
+                float r = wmax[buf][i][(threadIdx.x & 31) % B::kWarps];
+#pragma unroll
+                for (int o = B::kWarps / 2; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+                m[i] = r;
+            }
+            buf ^= 1;               // the next maxima go elsewhere: these may still be read
+        };
+        block_max();
+        float top = m[0];
+#pragma unroll
+        for (int i = 1; i < B::kKvHeads; ++i) top = fmaxf(top, m[i]);
+        if (top == INFINITY) {
+#pragma unroll
+            for (int i = 0; i < B::kKvHeads; ++i) {
+                drop_infinities(y[i].a);
+                drop_infinities(y[i].b);
+            }
+            block_max();
+        }
+        const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows && page_ok;
+#pragma unroll
+        for (int i = 0; i < B::kKvHeads; ++i) {
+            const int h = u.part + i * kv_parts;
+            if (!page_ok || h >= a.Hkv) continue;
+            const PageScale ps = page_scale(lo, old[i], m[i]);
+            if (!ps.ok) {
+                if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+                continue;
+            }
+            if (threadIdx.x == 0 && !ps.keep) scale[h] = ps.s;
+            uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ((head0 + h) * kPageRows + slot) * D + 8 * l;
+            uint2 c = make_uint2(0u, 0u), c2 = c;
+            if (fresh) {
+                c = to_codes(y[i].a, 1.f / ps.s);
+                c2 = to_codes(y[i].b, 1.f / ps.s);
+            } else if (slot < lo && (!ps.keep || pool)) {
+                c = *reinterpret_cast<const uint2*>(row);
+                c2 = *reinterpret_cast<const uint2*>(row + D / 2);
+                if (!ps.keep) {
+                    c = to_codes(from_codes(c), old[i] * (1.f / ps.s));
+                    c2 = to_codes(from_codes(c2), old[i] * (1.f / ps.s));
+                }
+            }
+            if (fresh || (slot < lo && !ps.keep)) {
+                *reinterpret_cast<uint2*>(row) = c;
+                *reinterpret_cast<uint2*>(row + D / 2) = c2;
+            }
+            if (pool) {
+                // the mean key of the filled page, in the order of page_rows, where the stage's rows were
+                static_assert(kPageRows * D * 4 <= B::kStageBytes, "a head's rows in fp32");
+                float(*red)[D] = reinterpret_cast<float(*)[D]>(ring_s + (st ^ 1) * B::kStageBytes);
+                store_sum<D>(red[slot], l, Row{from_codes(c), from_codes(c2)});
+                __syncthreads();
+                if (threadIdx.x < D) {
+                    float total = 0.f;
+                    for (int j = 0; j < kSumRows<D>; ++j) {
+                        float part = 0.f;
+#pragma unroll
+                        for (int r = 0; r < kPageRows / kSumRows<D>; ++r) part += red[j + r * kSumRows<D>][threadIdx.x];
+                        total += part;
+                    }
+                    a.kpool[(head0 + h) * D + threadIdx.x] = total * ps.s * (1.f / kPageRows);
+                }
+                __syncthreads();    // read before the next head's rows, or the stage's next copies
+            }
+        }
+        cur = next;
+    }
+    copy_wait<0>();
+    flag_sequences(a);
 }
 
 template <int D, bool kQ8>
 cudaError_t go(const AppendArgs& a, cudaStream_t st) {
     constexpr long long kSlots = kThreads / HeadRow<D>::kLanes;
-    const long long items = append_items(a);
     cudaError_t e;
     if (a.max_new == 1) {
         constexpr long long kTokenSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
         const long long q_ctas = a.q != nullptr ? (a.T * a.Hq + kTokenSlots - 1) / kTokenSlots : 0;
+        const long long items = 2LL * a.N * a.Hkv;
         e = launch_dependent(append_token_kernel<D, kQ8>, dim3((unsigned)(q_ctas + (items + kCtaWarps - 1) / kCtaWarps)),
                              kTokenThreads, 0, st, a, (uint32_t)q_ctas);
         if (e == cudaSuccess) count_launches(1);
         return e;
     }
+    const long long blocks = (long long)seq_tile_base((int)a.T, a.N) + 1;       // tile indices
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
-    const long long q_parts = a.q != nullptr ? parts_of(a.Hq, kHeads) : 0, most = (long long)kCtas * sms;
+    const long long q_parts = a.q != nullptr ? parts_of(a.Hq, kHeads) : 0;
     if constexpr (kQ8) {
-        const long long q_units = a.T * q_parts, batches = (q_units + kSlots - 1) / kSlots;
-        e = launch_dependent(append_tiles_kernel<D>, dim3((unsigned)std::min(batches + items, most)), kThreads, 0, st, a,
-                             (uint32_t)q_units, (uint32_t)batches, (uint32_t)items);
+        using B = Blocks<D>;
+        e = cudaFuncSetAttribute(append_blocks_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, B::kSmem);
+        if (e != cudaSuccess) return e;
+        const long long kv_works = blocks * 2 * parts_of(a.Hkv, B::kKvHeads), q_units = a.T * q_parts;
+        const long long works = kv_works + (q_units + kPageRows - 1) / kPageRows;
+        e = launch_dependent(append_blocks_kernel<D>, dim3((unsigned)std::min(works, (long long)B::kCtas * sms)), B::kThreads,
+                             B::kSmem, st, a, (uint32_t)kv_works, (uint32_t)q_units, (uint32_t)works);
     } else {
         const long long units = a.T * (q_parts + 2 * parts_of(a.Hkv, kHeads));
-        e = launch_dependent(append_rows_kernel<D>, dim3((unsigned)std::min((units + kSlots - 1) / kSlots, most)), kThreads, 0,
+        e = launch_dependent(append_rows_kernel<D>, dim3((unsigned)std::min((units + kSlots - 1) / kSlots, (long long)kCtas * sms)), kThreads, 0,
                              st, a, (uint32_t)q_parts, (uint32_t)units);
         if (e == cudaSuccess && a.kpool != nullptr) {
             count_launches(1);
             constexpr int kCtaWarps = kThreads / 32;
-            const long long heads = items / 2;
+            const long long heads = blocks * a.Hkv;
             e = launch_dependent(pool_filled_kernel<D>, dim3((unsigned)((heads + kCtaWarps - 1) / kCtaWarps)), kThreads, 0, st, a,
                                  (uint32_t)heads);
         }
@@ -724,10 +702,6 @@ cudaError_t go(const AppendArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
-
-long long append_items(const AppendArgs& a) {
-    return (a.max_new == 1 ? (long long)a.N : (long long)seq_tile_base((int)a.T, a.N) + 1) * a.Hkv * 2;
-}
 
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t st) {
     if (a.k_scale != nullptr) return D == 128 ? go<128, true>(a, st) : go<64, true>(a, st);

@@ -3,7 +3,7 @@
 // launched this way calls after_previous() before it touches memory, which
 // waits until that kernel has finished and its writes are visible: only the
 // placement of the CTAs comes early. In a stream of calls this saves one to two
-// microseconds a kernel (a ragged append 22.5 -> 20.2 us). kEarly = false is for
+// microseconds a kernel (a ragged append 20.5 -> 18.5 us). kEarly = false is for
 // kernels that lose by it: early CTAs take the room that the previous kernel
 // leaves, so that not every SM gets its share of a persistent grid (norm +
 // rotation of 8k tokens, captured: 30.3 us, early 31.7).

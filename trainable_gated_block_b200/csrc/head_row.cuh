@@ -193,19 +193,6 @@ struct Turn {
     }
 };
 
-// One row alone, with the weights at hand: n = x (w r), then the turn.
-__device__ __forceinline__ Row norm_turn(const Row& x, const Row& w, float r, const Angles& g) {
-    const f2 rr = f2_pack(r, r), neg = f2_pack(-1.f, -1.f);
-    Row y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f2 a = f2_mul(x.a.v[i], f2_mul(w.a.v[i], rr)), b = f2_mul(x.b.v[i], f2_mul(w.b.v[i], rr));
-        y.a.v[i] = f2_fma(a, g.c.v[i], f2_mul(b, f2_mul(g.s.v[i], neg)));
-        y.b.v[i] = f2_fma(b, g.c.v[i], f2_mul(a, g.s.v[i]));
-    }
-    return y;
-}
-
 // 16 bytes from global to shared memory without a register (zeroes without
 // `live`); each thread copies and later reads its own pieces only, so that the
 // groups need no barrier.

@@ -141,7 +141,6 @@ struct AppendArgs {
     void* q_out; void* k_out; void* k_cache; void* v_cache; float* k_scale; float* v_scale; float* kpool;
     int* status;
 };
-long long append_items(const AppendArgs& a);     // (sequence, block, KV head) tiles of K and V
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t st);
 
 // One warp waiting (bounded) on a barrier nothing arrives on: records a timeout in *status.

@@ -51,10 +51,12 @@ struct Bwd {
     static constexpr int kSmem = kRing > kSlots * D * 4 ? kRing : kSlots * D * 4;
 };
 
-// Units 0 .. q_units - 1 are the queries', the others the keys'.
+// A token's units lie one after the other, its queries' and its keys', so that the
+// CTAs that run together read whole rows of a fused projection (all queries' units
+// first, then the keys': 112.3 instead of 106.7 us for 32k tokens).
 template <typename T, int D>
 __global__ void __launch_bounds__(Fwd<T, D>::kThreads, Fwd<T, D>::kCtas)
-norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __restrict__ q_out, T* __restrict__ k_out) {
+norm_rope_kernel(const NormRopeArgs a, uint32_t units, T* __restrict__ q_out, T* __restrict__ k_out) {
     using S = Fwd<T, D>;
     constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16, kStage = S::kHeads * kRow;    // bytes from row to row, stage to stage
     extern __shared__ __align__(16) uint8_t smem[];
@@ -62,17 +64,17 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
     const uint32_t ring = sm100::smem_u32(smem) + threadIdx.x * 16;
     const int l = threadIdx.x % HeadRow<D>::kLanes;
     const uint32_t first = blockIdx.x * S::kSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * S::kSlots;
-    const uint32_t parts_q = parts_of(a.Hq, S::kHeads), parts_k = parts_of(a.Hkv, S::kHeads);
+    const uint32_t parts_q = parts_of(a.Hq, S::kHeads), parts_k = parts_of(a.Hkv, S::kHeads), per = parts_q + parts_k;
 
     auto issue = [&](uint32_t u, uint32_t st) {
         if (u < units) {
-            const bool is_k = u >= q_units;
-            const int H = is_k ? a.Hkv : a.Hq;
-            const uint32_t parts = is_k ? parts_k : parts_q, w = is_k ? u - q_units : u, t = w / parts;
+            const uint32_t t = u / per, j = u - t * per;
+            const bool is_k = j >= parts_q;
+            const int H = is_k ? a.Hkv : a.Hq, parts = (int)(is_k ? parts_k : parts_q), h0 = (int)(is_k ? j - parts_q : j);
             const T* src = static_cast<const T*>(is_k ? a.k : a.q) + (long long)t * (is_k ? a.ld_k : a.ld_q);
 #pragma unroll
             for (int i = 0; i < S::kHeads; ++i) {
-                const int h = (int)(w - t * parts + i * parts);
+                const int h = h0 + i * parts;
                 copy_row<T, D, S::kThreads>(ring + st * kStage + i * kRow, src + (h < H ? h : 0) * D, l, h < H);
             }
         }
@@ -84,9 +86,10 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
     for (int s = 0; s < S::kStages; ++s, next += step) issue(next, s);
     // (no sum here passes 2^32: units is below 2^31)
     for (uint32_t base = blockIdx.x * S::kSlots, u = first; base < units; base += step, u += step) {
-        const bool live = u < units, is_k = u >= q_units;
-        const int H = is_k ? a.Hkv : a.Hq;
-        const uint32_t parts = is_k ? parts_k : parts_q, w = !live ? 0 : is_k ? u - q_units : u, t = w / parts;
+        const bool live = u < units;
+        const uint32_t t = live ? u / per : 0, j = live ? u - t * per : 0;
+        const bool is_k = j >= parts_q;
+        const int H = is_k ? a.Hkv : a.Hq, parts = (int)(is_k ? parts_k : parts_q), h0 = (int)(is_k ? j - parts_q : j);
         const T* weight = static_cast<const T*>(is_k ? a.k_weight : a.q_weight);
         const int pos = live ? token_pos(a, t) : -1;
         const Turn turn(load_angles<T, D>(a.table, max(pos, 0), l), load_weight<T, D>(weight, l));
@@ -94,7 +97,7 @@ norm_rope_kernel(const NormRopeArgs a, uint32_t q_units, uint32_t units, T* __re
         copy_wait<S::kStages - 1>();
 #pragma unroll
         for (int i = 0; i < S::kHeads; ++i) {
-            const int h = (int)(w - t * parts + i * parts);
+            const int h = h0 + i * parts;
             const Row x = read_row<T, S::kThreads>(ring + st * kStage + i * kRow);
             Row y = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
             if (pos < 0) y = Row{};
@@ -277,11 +280,11 @@ unsigned grid_for(long long units, int slots, int ctas) {
 template <typename T, int D>
 cudaError_t fwd(const NormRopeArgs& a, void* q_out, void* k_out, cudaStream_t st) {
     using S = Fwd<T, D>;
-    const uint32_t uq = (uint32_t)a.T * parts_of(a.Hq, S::kHeads), n = uq + (uint32_t)a.T * parts_of(a.Hkv, S::kHeads);
+    const uint32_t n = (uint32_t)a.T * (parts_of(a.Hq, S::kHeads) + parts_of(a.Hkv, S::kHeads));
     cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent<false>(norm_rope_kernel<T, D>, dim3(grid_for(n, S::kSlots, S::kCtas)), S::kThreads, S::kSmem, st, a, uq, n,
-                         static_cast<T*>(q_out), static_cast<T*>(k_out));
+    e = launch_dependent<false>(norm_rope_kernel<T, D>, dim3(grid_for(n, S::kSlots, S::kCtas)), S::kThreads, S::kSmem, st, a, n,
+                                static_cast<T*>(q_out), static_cast<T*>(k_out));
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
