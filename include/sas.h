@@ -366,6 +366,8 @@ size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
  *            and 2^120 for every page that is read; any other scale is flagged and
  *            its block skipped, like a bad page id.
  * kv_len     as in sas_decode_paged; 0 is a padding entry: o 0, lse -inf, not flagged.
+ * log_gate   -inf (or the lowest fp32 value) leaves its block out, whatever its page
+ *            holds. A block that idx names twice is attended twice.
  * Other arguments as in sas_decode_paged. Logits, softmax sums and accumulators are
  * fp32; probabilities are rounded to fp16 in front of the value product. A sequence
  * without a readable block gets o 0 and lse -inf.
@@ -389,7 +391,8 @@ sas_status sas_decode_paged_q8(const void *q, const void *k_cache, const void *v
  * row t at position p:
  *   n = x * rsqrt(mean(x^2) + eps) * weight,
  *   y[i] = n[i] c[i] - n[i + D/2] s[i],  y[i + D/2] = n[i + D/2] c[i] + n[i] s[i]
- * for i < D/2, with c, s from row p of the table; fp32 arithmetic, rounded once.
+ * for i < D/2, with c, s from row p of the table; fp32 arithmetic, rounded once (with
+ * weights, the squares of a row must not sum up beyond fp32's range).
  *
  * dtype      SAS_BF16 or SAS_F32: q, k, the weights and the outputs.
  * q, k       device [T, Hq, D], [T, Hkv, D]; each token's heads are contiguous, ld_q and

@@ -114,7 +114,9 @@ def decode_q8(q, k_codes, v_codes, k_scale, v_scale, page_table, kv_len, idx, cn
             continue
         c = (int(kv_len[n]) - 1) // BLOCK
         for h in range(Hkv):
-            blocks = [(int(pt[n, j]), BLOCK, gate[n, h, i]) for i, j in enumerate(idx[n, h, :cnt[n, h]])]
+            # a gate of -inf leaves its block out (its weight is 0, and so is its part of the bound)
+            blocks = [(int(pt[n, j]), BLOCK, gate[n, h, i]) for i, j in enumerate(idx[n, h, :cnt[n, h]])
+                      if gate[n, h, i] != -np.inf]
             blocks.append((int(pt[n, c]), int(kv_len[n]) - c * BLOCK, 0.0))
             kcode = np.concatenate([kc[p, h, :r] for p, r, _ in blocks])
             vcode = np.concatenate([vc[p, h, :r] for p, r, _ in blocks])

@@ -174,6 +174,31 @@ def test_gates_that_close_blocks():
     _check(_run(x), _ref(y))
 
 
+def test_a_closed_block_is_left_out_whatever_it_holds():
+    x = _make([300, 450, 200], 4, 2, 3, seed=12)
+    x["log_gate"][1, :, 1] = -math.inf
+    x["log_gate"][2] = -math.inf
+    x["log_gate"][2, :, 1] = torch.finfo(torch.float32).min
+    want = _run(x)
+    y = dict(x, log_gate=x["log_gate"].clone())
+    y["log_gate"][2] = -math.inf
+    _check(want, _ref(y))
+    for n, i in ((1, 1), (2, 0), (2, 1), (2, 2)):
+        for h in range(2):
+            page = int(x["page_table"][n, x["idx"][n, h, i]])
+            for cache in ("k_cache", "v_cache"):
+                x[cache].view(torch.uint8)[page, h, 5:40] = 0x7f          # NaN
+    got = _run(x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_block_named_twice_counts_twice():
+    x = _make([400, 1000], 8, 2, 4, seed=13)
+    x["idx"][:, :, 2] = x["idx"][:, :, 1]
+    x["log_gate"][:, :, 2] = x["log_gate"][:, :, 1] - 0.5
+    _check(_run(x), _ref(x))
+
+
 def test_nan_in_a_query_or_a_key_reaches_its_rows_only():
     x = _make([64 * 3 + 1, 64 * 3 + 1], 8, 2, 3, seed=10)
     ref = _ref(x)

@@ -57,7 +57,7 @@ struct Block {              // a resolved block of a warp's stream
     int row0;               // first cache row of its tile
     int tokens;             // rows to copy; 0: nothing to read
     int item;
-    int nvalid;             // rows to attend: tokens, or 0 when the scales are out of range
+    int nvalid;             // rows to attend: tokens, or 0 when the gate is closed or a scale out of range
     float bias;             // gate + log2(vs), log2 units
     float ks, inv_vs;
     int pad;
@@ -190,8 +190,8 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
 __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b) {
     const bool ok = scale_ok(r.ks) && scale_ok(r.vs);
     if (!ok) flag_status(p.status, kStatusBadData);
-    b.nvalid = ok ? r.tokens : 0;
     b.bias = r.gate * kLog2e + log2f(r.vs);
+    b.nvalid = ok && b.bias != -INFINITY ? r.tokens : 0;     // behind a closed gate a NaN must not reach the sums
     b.ks = r.ks;
     b.inv_vs = 1.f / r.vs;
 }
