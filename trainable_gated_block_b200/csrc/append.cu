@@ -20,15 +20,19 @@
 // Each thread prefetches its pieces of the next unit with cp.async.
 //
 // Measured on one B200 (32/8 heads of 128): one token of one sequence 3.4 us, of 64
-// sequences into 8-bit pages 6.9, two of which fill a page, of 256 sequences 9.2
-// (22.5 with a CTA for each row); prompts of 8k and 32k tokens into bf16 pages 36.8
-// and 127.5 us (86 and 100% of the copy rate; as 64-row tiles of one head 42.5 and
-// 147), into 8-bit pages 41.7 and 154 (70 and 76%): the blocks' barrier leaves the
-// latencies of one CTA's 16 warps in a row.
+// sequences into 8-bit pages 4.9, two of which fill a page, of 256 sequences 6.7
+// (22.5 with a CTA for each row; 6.9 and 8.8 where the filled pages' rows met in
+// shared memory instead of by shuffles, without their loads in flight together);
+// prompts of 8k and 32k tokens into bf16 pages 36.5 and 127.5 us (87 and 100% of the
+// copy rate; as 64-row tiles of one head 42.5 and 147; 41 and 141 with the pages'
+// mean keys), into 8-bit pages 41.4 and 153 (70 and 76%): the blocks' barrier leaves
+// the latencies of one CTA's 16 warps in a row. (Reading the rows twice instead of
+// holding them in registers, for two or three CTAs an SM: 46.8 and 75 us at 8k.)
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dependent.cuh"
 #include "head_row.cuh"
@@ -134,56 +138,106 @@ __device__ __forceinline__ PageScale page_scale(int lo, float old, float m) {
     return p;
 }
 
-// The mean key of a filled page is summed in one order by both kernels: the
-// rows j, j + kSumRows, ... for each j, then these sums by j.
+// The mean key of a filled page is summed in one order by all kernels: for each
+// warp w of kSlots row slots the rows slot and slot + kSlots of its slots, these over
+// the warp's slots (sum_slots), and the sums by w.
+constexpr int kSlots = 32;                  // row slots of a page: each has kPageRows / kSlots rows
+constexpr int kSlotRows = kPageRows / kSlots;
+
+// Sums of a row over the warp's row slots. Each step halves what a lane keeps: it
+// ends with kKept pairs of neighbouring dimensions, from sum_dim on.
 template <int D>
-constexpr int kSumRows = D == 128 ? 16 : 32;
+struct SlotSum {
+    static constexpr int kSteps = D == 128 ? 2 : 3, kKept = 8 >> kSteps;
+    f2 v[kKept];
+};
+template <int D>
+__device__ __forceinline__ int sum_dim(int lane) {
+    const int l = lane % HeadRow<D>::kLanes, grp = lane / HeadRow<D>::kLanes;
+    return (grp & 1) * (D / 2) + 8 * l + (grp >> 1 & 1) * 4 + (D == 64 ? (grp >> 2) * 2 : 0);
+}
+template <int D>
+__device__ __forceinline__ SlotSum<D> sum_slots(int lane, const Row& r) {
+    f2 v[8] = {r.a.v[0], r.a.v[1], r.a.v[2], r.a.v[3], r.b.v[0], r.b.v[1], r.b.v[2], r.b.v[3]};
+#pragma unroll
+    for (int k = 0; k < SlotSum<D>::kSteps; ++k) {
+        const int o = HeadRow<D>::kLanes << k;
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < (4 >> k); ++i) {
+            const f2 keep = up ? v[i + (4 >> k)] : v[i], give = up ? v[i] : v[i + (4 >> k)];
+            v[i] = f2_add(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+    SlotSum<D> s;
+#pragma unroll
+    for (int i = 0; i < SlotSum<D>::kKept; ++i) s.v[i] = v[i];
+    return s;
+}
 
 // The rare work on the rows of a page and head, by one warp: the codes of the
 // first `grown` rows times `ratio`, and with `pool` the mean of the page's 64 keys
-// (times their scale `unit`). Rows from `rows` on are not looked at. `red`: the
-// warp's [kSumRows][D] floats.
+// (times their scale `unit`). Rows from `rows` on are not looked at.
 template <int D, bool kQ8>
 __device__ __forceinline__ void page_rows(const AppendArgs& a, bool is_v, int page, int h, int rows, int grown, float ratio,
-                                          float unit, bool pool, float (*red)[D]) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp;
+                                          float unit, bool pool) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp, kRounds = kSlots / kPerWarp;
     const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
     const long long head = (long long)page * a.Hkv + h, tile0 = head * kPageRows;
+    SlotSum<D> mean{};
+    // the loads of four rounds are in flight together
+    constexpr int kAt = 4;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kRounds; k0 += kAt) {
+        using Piece = typename std::conditional<kQ8, uint2, uint4>::type;
+        Piece c[kAt][kSlotRows][2];
+        auto at = [&](int k, int i) { return kSlots * i + kPerWarp * (k0 + k) + grp; };
+        auto ptr = [&](int r) {
+            return static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ((tile0 + r) * D + 8 * l) * (kQ8 ? 1 : 2);
+        };
+        constexpr int kHalf = D / 2 * (kQ8 ? 1 : 2);            // bytes
 #pragma unroll
-    for (int k = 0; k < kSumRows<D> / kPerWarp; ++k) {
-        Row sum{};
+        for (int k = 0; k < kAt; ++k)
 #pragma unroll
-        for (int i = 0; i < kPageRows / kSumRows<D>; ++i) {
-            const int r = grp + kPerWarp * k + kSumRows<D> * i;
-            if (r >= rows) continue;
-            if (kQ8) {
-                uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (tile0 + r) * D + 8 * l;
-                uint2 c = *reinterpret_cast<const uint2*>(row), c2 = *reinterpret_cast<const uint2*>(row + D / 2);
-                if (r < grown) {
-                    *reinterpret_cast<uint2*>(row) = c = to_codes(from_codes(c), ratio);
-                    *reinterpret_cast<uint2*>(row + D / 2) = c2 = to_codes(from_codes(c2), ratio);
+            for (int i = 0; i < kSlotRows; ++i) {
+                const int r = at(k, i);
+                c[k][i][0] = c[k][i][1] = Piece{};
+                if (r < rows) {
+                    c[k][i][0] = *reinterpret_cast<const Piece*>(ptr(r));
+                    c[k][i][1] = *reinterpret_cast<const Piece*>(ptr(r) + kHalf);
                 }
-                if (pool) {
-                    add(sum.a, from_codes(c));
-                    add(sum.b, from_codes(c2));
-                }
-            } else {
-                const bf16* row = static_cast<const bf16*>(a.k_cache) + (tile0 + r) * D + 8 * l;
-                const uint4 c[1] = {*reinterpret_cast<const uint4*>(row)}, c2[1] = {*reinterpret_cast<const uint4*>(row + D / 2)};
-                add(sum.a, Raw8<bf16>::get(c));
-                add(sum.b, Raw8<bf16>::get(c2));
             }
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+            Row row[kSlotRows];
+#pragma unroll
+            for (int i = 0; i < kSlotRows; ++i) {
+                if constexpr (kQ8) {
+                    const int r = at(k, i);
+                    if (r < grown) {
+                        *reinterpret_cast<uint2*>(ptr(r)) = c[k][i][0] = to_codes(from_codes(c[k][i][0]), ratio);
+                        *reinterpret_cast<uint2*>(ptr(r) + kHalf) = c[k][i][1] = to_codes(from_codes(c[k][i][1]), ratio);
+                    }
+                    row[i] = {from_codes(c[k][i][0]), from_codes(c[k][i][1])};
+                } else {
+                    const uint4 lo[1] = {c[k][i][0]}, hi[1] = {c[k][i][1]};
+                    row[i] = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
+                }
+            }
+            if (!pool) continue;
+            static_assert(kSlotRows == 2, "rows of a slot");
+            add(row[0].a, row[1].a);
+            add(row[0].b, row[1].b);
+            const SlotSum<D> s = sum_slots<D>(lane, row[0]);
+#pragma unroll
+            for (int i = 0; i < SlotSum<D>::kKept; ++i) mean.v[i] = f2_add(mean.v[i], s.v[i]);
         }
-        if (pool) store_sum<D>(red[grp + kPerWarp * k], l, sum);
     }
     if (!pool) return;
-    __syncwarp();
-    for (int d = lane; d < D; d += 32) {
-        float m = 0.f;
-#pragma unroll 16
-        for (int i = 0; i < kSumRows<D>; ++i) m += red[i][d];
-        a.kpool[head * D + d] = m * unit * (1.f / kPageRows);
-    }
+    const f2 u = f2_pack(unit, unit), n = f2_pack(1.f / kPageRows, 1.f / kPageRows);
+    f2* out = reinterpret_cast<f2*>(a.kpool + head * D + sum_dim<D>(lane));
+#pragma unroll
+    for (int i = 0; i < SlotSum<D>::kKept; ++i) out[i] = f2_mul(f2_mul(mean.v[i], u), n);
 }
 
 // ------------------------------------------------------------------ single tokens
@@ -210,9 +264,9 @@ __device__ __forceinline__ void token_q(const AppendArgs& a, uint32_t u) {
 
 // The new row of one (sequence, KV head) of K or of V, by one warp: its first
 // D / 16 lanes hold the row, the whole warp does the rare work on the page's
-// older rows. `red`: the warp's [kSumRows][D] floats.
+// older rows.
 template <int D, bool kQ8>
-__device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float (*red)[D]) {
+__device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u) {
     constexpr int kLanes = HeadRow<D>::kLanes;
     const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
     if (u >= 2u * a.N * a.Hkv) return;
@@ -277,18 +331,17 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u, float 
     const bool grown = kQ8 && t.lo > 0 && !ps.keep, pool = !is_v && a.kpool != nullptr && t.lo == kPageRows - 1;
     if (!grown && !pool) return;
     __syncwarp();                                   // the new row is written
-    page_rows<D, kQ8>(a, is_v, page, h, t.lo + pool, grown ? t.lo : 0, old * (1.f / ps.s), ps.s, pool, red);
+    page_rows<D, kQ8>(a, is_v, page, h, t.lo + pool, grown ? t.lo : 0, old * (1.f / ps.s), ps.s, pool);
 }
 
 template <int D, bool kQ8>
 __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const AppendArgs a, uint32_t q_ctas) {
-    constexpr int kSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
-    __shared__ __align__(16) float red[kCtaWarps][kSumRows<D>][D];
+    constexpr int kCtaSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
     after_previous();
     if (blockIdx.x < q_ctas)
-        token_q<D>(a, blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes);
+        token_q<D>(a, blockIdx.x * kCtaSlots + threadIdx.x / HeadRow<D>::kLanes);
     else
-        token_kv<D, kQ8>(a, (blockIdx.x - q_ctas) * kCtaWarps + threadIdx.x / 32, red[threadIdx.x / 32]);
+        token_kv<D, kQ8>(a, (blockIdx.x - q_ctas) * kCtaWarps + threadIdx.x / 32);
 }
 
 // ------------------------------------------------------------------ prompts
@@ -383,13 +436,13 @@ constexpr int kStageBytes = 2 * kHeads * kThreads * 16;
 // Units of queries, keys, and values, which are copied as they are.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const AppendArgs a, uint32_t q_parts, uint32_t units) {
-    constexpr int kSlots = kThreads / HeadRow<D>::kLanes, kRow = 2 * kThreads * 16;
+    constexpr int kCtaSlots = kThreads / HeadRow<D>::kLanes, kRow = 2 * kThreads * 16;
     __shared__ __align__(16) uint8_t ring_s[kStages * kStageBytes];
     after_previous();
     const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
     const int l = threadIdx.x % HeadRow<D>::kLanes;
     const uint32_t kv_parts = parts_of(a.Hkv, kHeads), per = q_parts + 2 * kv_parts;
-    const uint32_t first = blockIdx.x * kSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * kSlots;
+    const uint32_t first = blockIdx.x * kCtaSlots + threadIdx.x / HeadRow<D>::kLanes, step = gridDim.x * kCtaSlots;
 
     SeqAt seq;
     auto unit_at = [&](uint32_t u) {
@@ -407,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
     Unit cur = unit_at(first);
     issue<D, kThreads, kHeads>(a, cur, ring);
     uint32_t st = 0;
-    for (uint32_t base = blockIdx.x * kSlots, u = first; base < units; base += step, u += step) {
+    for (uint32_t base = blockIdx.x * kCtaSlots, u = first; base < units; base += step, u += step) {
         const Unit next = unit_at(u + step);
         issue<D, kThreads, kHeads>(a, next, ring + (st ^ 1) * kStageBytes);
         const bool is_q = cur.kind == kQ, is_v = cur.kind == kV;
@@ -447,20 +500,48 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
     flag_sequences(a);
 }
 
-// The mean key of every page that the call has filled: a warp for each (block, KV head).
+// The mean key of every page that the call has filled, in the order of page_rows: a CTA
+// for each (block, KV head), each warp with its share of the rounds, so that the
+// tile's loads are all in flight together.
 template <int D>
-__global__ void __launch_bounds__(kThreads) pool_filled_kernel(const AppendArgs a, uint32_t items) {
-    constexpr int kCtaWarps = kThreads / 32;
-    __shared__ __align__(16) float red[kCtaWarps][kSumRows<D>][D];
+__global__ void __launch_bounds__(kThreads) pool_filled_kernel(const AppendArgs a) {
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp, kRounds = kSlots / kPerWarp;
+    constexpr int kOfWarp = kRounds / (kThreads / 32);
+    __shared__ __align__(16) float red[kRounds][D];
     after_previous();
-    const uint32_t it = blockIdx.x * kCtaWarps + threadIdx.x / 32;
-    if (it >= items) return;
     SeqAt seq;
-    const PageTile t = seq.find_tile(a, it / a.Hkv);
+    const PageTile t = seq.find_tile(a, blockIdx.x / a.Hkv);
     if (t.hi != kPageRows || t.hi <= t.lo) return;
     const int page = seq.page(a, t.block);
     if (page < 0 || page >= a.num_pages) return;
-    page_rows<D, false>(a, false, page, (int)(it % a.Hkv), kPageRows, 0, 1.f, 1.f, true, red[threadIdx.x / 32]);
+    const int lane = threadIdx.x & 31, l = lane % kLanes, first = threadIdx.x / 32 * kOfWarp;
+    const long long head = (long long)page * a.Hkv + blockIdx.x % a.Hkv;
+    const bf16* rows = static_cast<const bf16*>(a.k_cache) + (head * kPageRows + first * kPerWarp + lane / kLanes) * D + 8 * l;
+    uint4 c[kOfWarp][kSlotRows][2][1];
+#pragma unroll
+    for (int k = 0; k < kOfWarp; ++k)
+#pragma unroll
+        for (int i = 0; i < kSlotRows; ++i) {
+            const bf16* row = rows + (k * kPerWarp + i * kSlots) * D;
+            c[k][i][0][0] = *reinterpret_cast<const uint4*>(row);
+            c[k][i][1][0] = *reinterpret_cast<const uint4*>(row + D / 2);
+        }
+#pragma unroll
+    for (int k = 0; k < kOfWarp; ++k) {
+        Row r = {Raw8<bf16>::get(c[k][0][0]), Raw8<bf16>::get(c[k][0][1])};
+        add(r.a, Raw8<bf16>::get(c[k][1][0]));
+        add(r.b, Raw8<bf16>::get(c[k][1][1]));
+        const SlotSum<D> s = sum_slots<D>(lane, r);
+        f2* to = reinterpret_cast<f2*>(&red[first + k][sum_dim<D>(lane)]);
+#pragma unroll
+        for (int i = 0; i < SlotSum<D>::kKept; ++i) to[i] = s.v[i];
+    }
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) total += red[k][threadIdx.x];
+    a.kpool[head * D + threadIdx.x] = total * (1.f / kPageRows);
 }
 
 // ------------------------------------------------------------------ prompts into 8-bit pages
@@ -637,16 +718,23 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
             if (pool) {
                 // the mean key of the filled page, in the order of page_rows, where the stage's rows were
                 static_assert(kPageRows * D * 4 <= B::kStageBytes, "a head's rows in fp32");
+                constexpr int kPerWarp = HeadRow<D>::kPerWarp;
                 float(*red)[D] = reinterpret_cast<float(*)[D]>(ring_s + (st ^ 1) * B::kStageBytes);
                 store_sum<D>(red[slot], l, Row{from_codes(c), from_codes(c2)});
                 __syncthreads();
                 if (threadIdx.x < D) {
                     float total = 0.f;
-                    for (int j = 0; j < kSumRows<D>; ++j) {
-                        float part = 0.f;
+#pragma unroll 2
+                    for (int g = 0; g < kSlots / kPerWarp; ++g) {
+                        float part[kPerWarp];
 #pragma unroll
-                        for (int r = 0; r < kPageRows / kSumRows<D>; ++r) part += red[j + r * kSumRows<D>][threadIdx.x];
-                        total += part;
+                        for (int r = 0; r < kPerWarp; ++r)
+                            part[r] = red[g * kPerWarp + r][threadIdx.x] + red[g * kPerWarp + r + kSlots][threadIdx.x];
+#pragma unroll
+                        for (int n = 1; n < kPerWarp; n *= 2)
+#pragma unroll
+                            for (int r = 0; r < kPerWarp; r += 2 * n) part[r] += part[r + n];
+                        total += part[0];
                     }
                     a.kpool[(head0 + h) * D + threadIdx.x] = total * ps.s * (1.f / kPageRows);
                 }
@@ -661,7 +749,6 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
 
 template <int D, bool kQ8>
 cudaError_t go(const AppendArgs& a, cudaStream_t st) {
-    constexpr long long kSlots = kThreads / HeadRow<D>::kLanes;
     cudaError_t e;
     if (a.max_new == 1) {
         constexpr long long kTokenSlots = kTokenThreads / HeadRow<D>::kLanes, kCtaWarps = kTokenThreads / 32;
@@ -686,15 +773,13 @@ cudaError_t go(const AppendArgs& a, cudaStream_t st) {
         e = launch_dependent(append_blocks_kernel<D>, dim3((unsigned)std::min(works, (long long)B::kCtas * sms)), B::kThreads,
                              B::kSmem, st, a, (uint32_t)kv_works, (uint32_t)q_units, (uint32_t)works);
     } else {
+        constexpr long long kCtaSlots = kThreads / HeadRow<D>::kLanes;
         const long long units = a.T * (q_parts + 2 * parts_of(a.Hkv, kHeads));
-        e = launch_dependent(append_rows_kernel<D>, dim3((unsigned)std::min((units + kSlots - 1) / kSlots, (long long)kCtas * sms)), kThreads, 0,
+        e = launch_dependent<false>(append_rows_kernel<D>, dim3((unsigned)std::min((units + kCtaSlots - 1) / kCtaSlots, (long long)kCtas * sms)), kThreads, 0,
                              st, a, (uint32_t)q_parts, (uint32_t)units);
         if (e == cudaSuccess && a.kpool != nullptr) {
             count_launches(1);
-            constexpr int kCtaWarps = kThreads / 32;
-            const long long heads = blocks * a.Hkv;
-            e = launch_dependent(pool_filled_kernel<D>, dim3((unsigned)((heads + kCtaWarps - 1) / kCtaWarps)), kThreads, 0, st, a,
-                                 (uint32_t)heads);
+            e = launch_dependent(pool_filled_kernel<D>, dim3((unsigned)(blocks * a.Hkv)), kThreads, 0, st, a);
         }
     }
     if (e == cudaSuccess) count_launches(1);
