@@ -8,6 +8,7 @@ fallback: if libsas.so is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -372,24 +373,37 @@ def _expect_rows(name, t, dtype, shape, dev) -> int:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the other tensors")
-    st = t.stride()
-    H, D = shape[-2:]
-    if st[-1] != 1 or (H > 1 and st[-2] != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return _token_stride(name, t, shape)
+
+
+def _token_stride(name, t, shape) -> int:
     if len(shape) == 3:
-        return st[0] if shape[0] > 1 else H * D
-    B, S = shape[:2]
-    if B > 1 and S > 1 and st[0] != S * st[1]:
-        raise ValueError(f"{name}: token rows must lie at one stride")
-    return st[1] if S > 1 else st[0] if B > 1 else H * D
+        T, H, D = shape
+        st, head, one = t.stride()
+        ld = st if T > 1 else H * D
+    else:
+        B, S, H, D = shape
+        seq, st, head, one = t.stride()
+        if B > 1 and S > 1 and seq != S * st:
+            raise ValueError(f"{name}: token rows must lie at one stride")
+        ld = st if S > 1 else seq if B > 1 else H * D
+    if one != 1 or (H > 1 and head != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return ld
 
 
 def _expect_current(dev: int):
     """The tensors' device must be the current CUDA device, whose stream the call goes to."""
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("tensors must be on the current CUDA device")
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(call: str, dev: int, *sizes) -> int:
+    """A call's workspace size: a function of the device and the sizes (asking the library takes 0.7 us)."""
+    return int(getattr(lib(), call)(*sizes))
 
 
 def _dense_like(t):
@@ -427,12 +441,12 @@ def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, i
     _expect_current(dev)
     sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
     o = torch.empty_like(q)
-    lse = q.new_empty((N, Hq), dtype=_F32T) if with_lse else None
+    lse = q.new_empty(N, Hq, dtype=_F32T) if with_lse else None
     if N == 0:
         return o, lse
-    L = lib()
-    ws, ws_bytes, workspace = _workspace(workspace, L.sas_decode_q8_workspace_size(N, Hq, Hkv, D, K), dev, q)
-    code = L.sas_decode_paged_q8(*ptrs, P, pt, max_pages, kv, N, Hq, Hkv, D, page_size, K, *sel, sm_scale, o.data_ptr(),
+    need = _workspace_bytes("sas_decode_q8_workspace_size", dev, N, Hq, Hkv, D, K)
+    ws, ws_bytes, workspace = _workspace(workspace, need, dev, q)
+    code = lib().sas_decode_paged_q8(*ptrs, P, pt, max_pages, kv, N, Hq, Hkv, D, page_size, K, *sel, sm_scale, o.data_ptr(),
                                  lse.data_ptr() if with_lse else None, ws, ws_bytes, _raw_stream(dev))
     if code:
         _check(code)
@@ -460,14 +474,19 @@ def _qk_args(q, k, table, q_weight, k_weight, positions, eps):
     q on, and T, Hq, Hkv, D and the device."""
     qs, ks = q.shape, k.shape
     n = len(qs)
-    if n not in (3, 4) or len(ks) != n or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
+    if n == 3 and len(ks) == 3:
+        (S, Hq, D), (Sk, Hkv, Dk) = qs, ks
+        T, same = S, Sk == S and Dk == D
+    elif n == 4 and len(ks) == 4:
+        (B, S, Hq, D), (Bk, Sk, Hkv, Dk) = qs, ks
+        T, same = B * S, Bk == B and Sk == S and Dk == D
+    else:
+        same = False
+    if not same:
         raise ValueError(f"q and k must be [T,H,D] or [B,S,H,D] with the same tokens, got {tuple(qs)}, {tuple(ks)}")
     dtype, dev = q.dtype, q.get_device()
-    Hq, D = qs[-2:]
-    Hkv, S = ks[-2], qs[-3]
-    T = S if n == 3 else S * qs[0]
     max_pos = table.shape[0]
-    ld_q, ld_k = _expect_rows("q", q, dtype, qs, dev), _expect_rows("k", k, dtype, ks, dev)
+    ld_q, ld_k = _token_stride("q", q, qs), _expect_rows("k", k, dtype, ks, dev)
     tab = _expect("table", table, _F32T, (max_pos, D), dev)
     w = _weight_ptrs(q_weight, k_weight, dtype, D, dev)
     pos = None
@@ -504,10 +523,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, table, q_weight=None, k_weight=None, 
     dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
     dwq = dwk = None
     if q_weight is not None:
-        dwq, dwk = q.new_empty((2, D), dtype=_F32T).unbind()
-    L = lib()
-    ws, ws_bytes, workspace = _workspace(workspace, L.sas_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D), dev, q)
-    code = L.sas_qk_norm_rope_bwd(code, *up, *args, dq.data_ptr(), dk.data_ptr(), _addr(dwq), _addr(dwk), ws, ws_bytes,
+        dwq, dwk = torch.empty_like(q_weight, dtype=_F32T), torch.empty_like(k_weight, dtype=_F32T)
+    need = _workspace_bytes("sas_qk_norm_rope_bwd_workspace_size", dev, T, Hq, Hkv, D)
+    ws, ws_bytes, workspace = _workspace(workspace, need, dev, q)
+    code = lib().sas_qk_norm_rope_bwd(code, *up, *args, dq.data_ptr(), dk.data_ptr(), _addr(dwq), _addr(dwk), ws, ws_bytes,
                                   _raw_stream(dev))
     if code:
         _check(code)
@@ -526,7 +545,9 @@ def _append(q8, q, k, v, table, k_cache, v_cache, scales, page_table, kv_len, q_
     dev = q.get_device()
     dt = _F8 if q8 else _BF16
     pages = (P, Hkv, page_size, D)
-    ld_q = _expect_rows("q", q, _BF16, (T, Hq, D), dev)
+    if q.dtype is not _BF16:
+        raise TypeError(f"q must be {_BF16}, got {q.dtype}")
+    ld_q = _token_stride("q", q, (T, Hq, D))
     ld_k = _expect_rows("k", k, _BF16, (T, Hkv, D), dev)
     ld_v = _expect_rows("v", v, _BF16, (T, Hkv, D), dev)
     tab = _expect("table", table, _F32T, (max_pos, D), dev)
