@@ -127,6 +127,14 @@ def test_enough_slots_for_the_many_warp_kernel():
     _check(_run(x), _ref(x))
 
 
+@pytest.mark.parametrize("Hq,Hkv,N,K", [(32, 8, 6, 31), (8, 8, 6, 32), (32, 8, 7, 31), (8, 1, 48, 5), (8, 1, 49, 5),
+                                        (5, 1, 1, 31), (6, 2, 3, 0), (7, 1, 2, 1)])
+def test_around_one_cluster_for_each_item(Hq, Hkv, N, K):
+    """Both sides of the border between a cluster for each item and the device's ranges: 48 items, K + 1 = 32."""
+    x = _make([(2100 + 300 * n) % 2600 for n in range(N)], Hq, Hkv, K, seed=30 + N + K)
+    _check(_run(x), _ref(x))
+
+
 def test_all_history_of_a_long_sequence():
     x = _make([64 * 300 + 5], 8, 2, 300, seed=5)
     _check(_run(x, sm_scale=0.03), _ref(x, 0.03))

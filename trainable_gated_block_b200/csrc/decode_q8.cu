@@ -27,10 +27,12 @@
 //       tile, the odd ones rows 8..15. P^T comes from S^T by movmatrix.
 // Nothing in the CTA waits for another warp: when a warp leaves an item it writes
 // its state (m, l, o) as one of the item's partials, and a combine kernel joins them.
+// Few items with few slots get a cluster of CTAs each instead, whose warps' partials
+// meet in its shared memory: one launch.
 //
-// Measured on one B200 (32/8 heads): eight 64k sequences with all history 171.7 us,
-// 6.26 TB/s of codes; 64 sequences at 8k-64k, K = 32: 55.6 us, 4.9 TB/s, of which
-// 8 us are the latency of a call that has one block for each warp (launch, the
+// Measured on one B200 (32/8 heads): eight 64k sequences with all history 171 us,
+// 6.28 TB/s of codes; 64 sequences at 8k-64k, K = 32: 55.6 us, 4.9 TB/s; one sequence
+// at 8k, K = 16: 7.1 us (by ranges and combine 8.6). Of the 55.6 us 8 are the latency of a call that has one block for each warp (launch, the
 // chain selection entry -> page -> tile, one block's math, the combine). A
 // variant with a producer warp, consumers that meet at each item's end and
 // one exp2f for each logit took 237 and 81.6 us: its math did not keep up.
@@ -64,13 +66,32 @@ struct Block {              // a resolved block of a warp's stream
 };
 constexpr int kList = 64;                           // two batches of a warp
 
+// Ten warps with one stage each hide the math better than four with three, but
+// cut the slots into more ranges, whose lengths differ by one. Measured (32/8
+// heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120 slots 66.3 /
+// 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten slots a
+// range on.
+constexpr int kManyWarps = 10, kFewWarps = 4;
+constexpr int kManySlots = 10;
+
+// Few items: a cluster of eight CTAs for each (three CTAs fit an SM), where their
+// warps have at most one slot each and all clusters are resident together. Clusters
+// stay within a GPC, so that not all places can be had: an eighth is left out.
+// Measured, cluster / ranges and combine (us, 8 KV heads): K = 16, one sequence 7.1 /
+// 8.6, five 8.9 / 10.3, six (48 items) 9.1 / 10.4, eight (more than fit) 15.8 / 11.4;
+// K = 31, one 7.4 / 8.3, six 9.9 / 11.8; K = 32, one 9.2 / 8.8, four 11.0 / 9.8. A
+// call from Python, where the second launch costs: 18.1 / 20.5.
+constexpr int kClusterCtas = 8;
+constexpr int kClusterWarps = kClusterCtas * kFewWarps, kClusterCtasPerSm = 3;
+
 // kWarps warps of one CTA per SM, kDepth ring stages each, and their shared memory.
 template <int kWarps, int kDepth>
 struct Shape {
     static constexpr uint32_t kOffList = kWarps * kDepth * kStageBytes;
     static constexpr uint32_t kOffBar = kOffList + kWarps * kList * sizeof(Block);
     static constexpr uint32_t kOffAbort = kOffBar + kWarps * kDepth * 8;
-    static constexpr uint32_t kSmem = kOffAbort + kWarps * 4 + 1024;       // + alignment slack
+    static constexpr uint32_t kOffMl = (kOffAbort + kWarps * 4 + 7) / 8 * 8;     // a warp's max and sum for each head
+    static constexpr uint32_t kSmem = kOffMl + kWarps * 8 * sizeof(float2) + 1024;       // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -92,6 +113,8 @@ struct Params {
     int nslot;              // partial slots per query head
     float* part_o;          // [N * Hq, nslot, D]
     float* part_ml;         // [N * Hq, nslot, 2]
+    __nv_bfloat16* o;       // [N, Hq, D]; lse [N, Hq] or null (kernel of one cluster an item)
+    float* lse;
     int* status;
 };
 
@@ -112,6 +135,21 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// Address of a cluster's CTA's counterpart of a shared memory address; loads from there.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int cta) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+// Every thread of every CTA of the cluster; what they wrote before is visible behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -196,16 +234,21 @@ __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b)
     b.inv_vs = 1.f / r.vs;
 }
 
-template <int kWarps, int kDepth>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+// kCluster = 1: the ranges of the whole device, whose partials go to the workspace.
+// Otherwise a cluster of kCluster CTAs for each item: its warps cut the item's K + 1
+// slots, and their partials meet in the cluster's shared memory.
+template <int kWarps, int kDepth, int kCluster>
+__global__ void __launch_bounds__(kWarps * 32, kCluster == 1 ? 1 : kClusterCtasPerSm)
 decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_k8, const __grid_constant__ CUtensorMap map_v8, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     after_previous();
-    const int range = warp * (int)gridDim.x + (int)blockIdx.x;
-    if (range >= p.ranges) return;
+    constexpr int kRanges = kWarps * kCluster;      // of an item
+    const int cta = (int)blockIdx.x % kCluster;
+    const int range = kCluster == 1 ? warp * (int)gridDim.x + (int)blockIdx.x : warp * kCluster + cta;
+    if (kCluster == 1 && range >= p.ranges) return;
 
     uint8_t* ring = smem + warp * kDepth * kStageBytes;
     Block* list = reinterpret_cast<Block*>(smem + Shape<kWarps, kDepth>::kOffList) + warp * kList;
@@ -220,11 +263,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     }
     __syncwarp();
 
-    const long long v1 = range_begin(range + 1, p.V, p.ranges);
-    long long v = range_begin(range, p.V, p.ranges);        // next slot to resolve
     const int Kp1 = p.K + 1;
+    const long long v0 = kCluster == 1 ? 0 : (long long)(blockIdx.x / kCluster) * Kp1;
+    const long long v1 = v0 + (kCluster == 1 ? range_begin(range + 1, p.V, p.ranges) : range_begin(range + 1, Kp1, kRanges));
+    long long v = v0 + (kCluster == 1 ? range_begin(range, p.V, p.ranges) : range_begin(range, Kp1, kRanges));  // next slot to resolve
     const int last_item = (int)((v1 - 1) / Kp1);
-    int cur_item = (int)(v / Kp1);
+    int cur_item = kCluster == 1 ? (int)(v / Kp1) : (int)(blockIdx.x / kCluster);
 
     const int grp = lane >> 2, tig = lane & 3;     // mma fragment coordinates
     // ldmatrix: this lane's row within 16 keys; chunk c of that row is at lofs ^ (c << 4) (c even; the odd
@@ -281,8 +325,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             ml[1] = 0.f;
         }
     };
-    auto write = [&](int item) {
-        const long long row = part_row(item);
+    // row g's partial: its max and sum to ml + g * stride, its accumulators to o_out + g * stride * D
+    auto write_to = [&](float2* ml, float* o_out, int stride) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -290,12 +334,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             if (l[e] != l[e]) m[e] = fmaxf(m[e], -1e30f);     // only NaN logits: the row is not an empty one
             const int g = 2 * tig + e;
             if (g >= p.G) continue;
-            const long long r = row + (long long)g * p.nslot;
-            if (grp == 0) *reinterpret_cast<float2*>(p.part_ml + r * 2) = make_float2(m[e], l[e]);
-            float* dst = p.part_o + r * kD + 2 * grp;
+            if (grp == 0) ml[(long long)g * stride] = make_float2(m[e], l[e]);
+            float* dst = o_out + (long long)g * stride * kD + 2 * grp;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) *reinterpret_cast<float2*>(dst + 16 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
         }
+    };
+    auto write = [&](int item) {
+        const long long row = part_row(item);
+        write_to(reinterpret_cast<float2*>(p.part_ml) + row, p.part_o + row * kD, p.nslot);
     };
 
     uint32_t found = 0, issued = 0, done = 0;      // blocks resolved, copied, consumed
@@ -451,8 +498,45 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         volatile int no_abort = 0;
         for (uint32_t k = done; k < issued; ++k) mbar_wait(&full[k % kDepth], (k / kDepth) & 1, &no_abort, nullptr);
     }
-    if (started) write(cur_item++);
-    for (; cur_item <= last_item; ++cur_item) write_empty(cur_item);
+    if constexpr (kCluster == 1) {
+        if (started) write(cur_item++);
+        for (; cur_item <= last_item; ++cur_item) write_empty(cur_item);
+    } else {
+        // the warp's partial into its ring, which is done with
+        static_assert(kRanges == 32 && kWarps * 32 == kD, "a lane for each partial, a thread for each dimension");
+        float2* ml = reinterpret_cast<float2*>(smem + Shape<kWarps, kDepth>::kOffMl);
+        if (started)
+            write_to(ml + warp * 8, reinterpret_cast<float*>(ring), 1);
+        else if (lane < p.G)
+            ml[warp * 8 + lane] = make_float2(-INFINITY, 0.f);
+        cluster_sync();
+        const int n = cur_item / p.Hkv, h = cur_item % p.Hkv;
+        for (int g = cta; g < p.G; g += kCluster) {
+            const uint32_t at = cluster_addr(smem_u32(ml + lane / kCluster * 8 + g), lane % kCluster);
+            const float wm = ld_cluster(at), wl = ld_cluster(at + 4);
+            float M = wm;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+            const float f = wm == -INFINITY ? 0.f : exp2f(wm - M);
+            const unsigned full_parts = __ballot_sync(0xffffffffu, wm != -INFINITY);
+            float L = wm == -INFINITY ? 0.f : wl * f, acc = 0.f;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+#pragma unroll 8
+            for (int i = 0; i < kRanges; ++i) {
+                // (an empty partial's place is read all the same, and not used)
+                const float x = ld_cluster(cluster_addr(smem_u32(smem + i / kCluster * kDepth * kStageBytes) + (g * kD + threadIdx.x) * 4,
+                                                        i % kCluster));
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                if (full_parts >> i & 1) acc = fmaf(x, fi, acc);
+            }
+            const bool none = M == -INFINITY;
+            const long long row = (long long)n * p.Hq + h * p.G + g;
+            p.o[row * kD + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : acc / L);
+            if (p.lse != nullptr && threadIdx.x == 0) p.lse[row] = none ? M : (M + log2f(L)) * kLn2;
+        }
+        cluster_sync();             // nobody leaves while its partials are read
+    }
 }
 
 // Joins the partials of one (sequence, query head): kGroups groups of threads
@@ -526,17 +610,9 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
     if (lse != nullptr && d == 0) lse[row] = none ? M : (M + log2f(L)) * kLn2;
 }
 
-// Ten warps with one stage each hide the math better than four with three, but
-// cut the slots into more ranges, whose lengths differ by one. Measured (32/8
-// heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120 slots 66.3 /
-// 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten slots a
-// range on.
-constexpr int kManyWarps = 10, kFewWarps = 4;
-constexpr int kManySlots = 10;
-
 struct Layout {
     long long V;
-    bool many;
+    bool many, cluster;
     int grid, ranges, nslot;
 };
 Layout layout(int N, int Hkv, int K) {
@@ -552,16 +628,18 @@ Layout layout(int N, int Hkv, int K) {
     const long long mn = r.V / r.ranges;                     // shortest range
     const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
     r.nslot = (int)(span < r.ranges ? span : r.ranges);
+    r.cluster = K + 1 <= kClusterWarps && (long long)N * Hkv * kClusterCtas <= kClusterCtasPerSm * sms * 7 / 8;
+    if (r.cluster) r.grid = N * Hkv * kClusterCtas;
     return r;
 }
 
-template <int kWarps, int kDepth>
+template <int kWarps, int kDepth, int kCluster = 1>
 cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params& p, cudaStream_t st) {
     constexpr int kSmem = (int)Shape<kWarps, kDepth>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<kWarps, kDepth>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const auto kernel = decode_q8_kernel<kWarps, kDepth, kCluster>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(decode_q8_kernel<kWarps, kDepth>, dim3(lay.grid), kWarps * 32, kSmem, st, map[0], map[1], map[2],
-                            map[3], p);
+    return launch_dependent<true, kCluster>(kernel, dim3(lay.grid), kWarps * 32, kSmem, st, map[0], map[1], map[2], map[3], p);
 }
 
 }  // namespace
@@ -604,7 +682,14 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     p.nslot = lay.nslot;
     p.part_o = part_o;
     p.part_ml = part_ml;
+    p.o = (__nv_bfloat16*)a.o;
+    p.lse = a.lse;
     p.status = a.status;
+    if (lay.cluster) {
+        const cudaError_t e = launch<kFewWarps, 1, kClusterCtas>(lay, map, p, st);
+        if (e == cudaSuccess) count_launches(1);
+        return e;
+    }
     cudaError_t e = lay.many ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
     if (e != cudaSuccess) return e;
     count_launches(1);
