@@ -127,10 +127,16 @@ def test_enough_slots_for_the_many_warp_kernel():
     _check(_run(x), _ref(x))
 
 
-@pytest.mark.parametrize("Hq,Hkv,N,K", [(32, 8, 6, 31), (8, 8, 6, 32), (32, 8, 7, 31), (8, 1, 48, 5), (8, 1, 49, 5),
-                                        (5, 1, 1, 31), (6, 2, 3, 0), (7, 1, 2, 1)])
-def test_around_one_cluster_for_each_item(Hq, Hkv, N, K):
-    """Both sides of the border between a cluster for each item and the device's ranges: 48 items, K + 1 = 32."""
+@pytest.mark.parametrize("Hq,Hkv,N,K", [
+    # one slot for each warp of a cluster of 32, 24, 16, 12, 8, 6, 4 and 3 warps; an empty selection
+    (32, 8, 6, 31), (8, 8, 1, 20), (8, 8, 12, 15), (8, 4, 2, 10), (28, 4, 1, 7), (4, 4, 1, 5), (5, 1, 1, 3), (7, 1, 2, 1),
+    (6, 2, 3, 0),
+    # more slots than warps; a second wave of clusters
+    (8, 8, 6, 32), (32, 8, 7, 31), (8, 1, 48, 5), (8, 1, 49, 5), (16, 8, 16, 20), (8, 8, 20, 18), (8, 8, 30, 13),
+    (16, 8, 40, 9), (8, 8, 96, 5), (8, 8, 130, 5),
+    # the device's ranges: few items with many slots, odd waves
+    (8, 8, 2, 40), (8, 8, 75, 6), (8, 8, 75, 24)])
+def test_every_way_to_cut_the_work(Hq, Hkv, N, K):
     x = _make([(2100 + 300 * n) % 2600 for n in range(N)], Hq, Hkv, K, seed=30 + N + K)
     _check(_run(x), _ref(x))
 

@@ -12,28 +12,32 @@
 // it), the weights are rounded to fp16 (2^-11 relative); logits, sums and
 // accumulators are fp32.
 //
-// HBM-bound design. The kept blocks of all (sequence, KV head) items lie end to
-// end, K + 1 slots each, cut into one contiguous range for each warp of the
-// device. A warp streams its range on its own: its lanes resolve 32 slots at a
-// time (selection entry, page, gate, scales), lane 0 copies the (page, head)
-// tiles, 8 KiB of K and 8 KiB of V, by TMA into the warp's ring, and the warp
-// does each block on mma.sync m16n8k16 with keys (or value dimensions) as the
-// 16 rows and the up to 8 query heads of the group as the 8 columns:
+// HBM-bound design. Each (sequence, KV head) item has K + 1 slots: its kept blocks and
+// the current one. The warps of a cluster of one to eight CTAs cut an item's slots
+// into contiguous ranges; a warp streams its range on its own: its lanes resolve 32
+// slots at a time (selection entry, page, gate, scales), lane 0 copies a (page, head)
+// tile, 8 KiB of K and 8 KiB of V, by TMA into the warp's stage, and the warp does
+// the block on mma.sync m16n8k16 with keys (or value dimensions) as the 16 rows
+// and the up to 8 query heads of the group as the 8 columns:
 //   S^T = K Q^T : A from ldmatrix over byte pairs. A lane gets four neighbouring
 //       dimensions of a key; the first two serve as the lane's low k pair, the
 //       others as its high pair, and Q is loaded in the same order.
 //   O^T = V^T P^T : A from ldmatrix.trans over byte pairs, which are two
 //       neighbouring dimensions of a key: the even ones become rows 0..7 of the
 //       tile, the odd ones rows 8..15. P^T comes from S^T by movmatrix.
-// Nothing in the CTA waits for another warp: when a warp leaves an item it writes
-// its state (m, l, o) as one of the item's partials, and a combine kernel joins them.
-// Few items with few slots get a cluster of CTAs each instead, whose warps' partials
-// meet in its shared memory: one launch.
+// No warp waits for another until its range is done. Then its state (m, l, o) is in
+// its shared memory, and the cluster joins its warps' states over distributed shared
+// memory: one launch, and nothing but the output is written. Twelve warps an SM, of
+// twelve other blocks, hide each other's copies and math.
+// Where clusters do not fill the device (few items with many slots, odd waves) all
+// items' slots lie end to end instead, cut into a range for each warp of the device;
+// a warp that leaves an item writes its state to the workspace, and a combine kernel
+// joins them.
 //
-// Measured on one B200 (32/8 heads): eight 64k sequences with all history 171 us,
-// 6.28 TB/s of codes; 64 sequences at 8k-64k, K = 32: 55.6 us, 4.9 TB/s; one sequence
-// at 8k, K = 16: 7.1 us (by ranges and combine 8.6). Of the 55.6 us 8 are the latency of a call that has one block for each warp (launch, the
-// chain selection entry -> page -> tile, one block's math, the combine). A
+// Measured on one B200 (32/8 heads): eight 64k sequences with all history 164 us, 6.57
+// TB/s of codes (by ranges 171); 64 sequences at 8k-64k, K = 32: 51.2 us, 5.3 TB/s (by
+// ranges 55.6); one sequence at 8k, K = 16: 6.8 us (8.6), the latency of a launch, the
+// chain selection entry -> page -> tile, one block's math and the join. A
 // variant with a producer warp, consumers that meet at each item's end and
 // one exp2f for each logit took 237 and 81.6 us: its math did not keep up.
 #include <cuda_fp16.h>
@@ -66,25 +70,19 @@ struct Block {              // a resolved block of a warp's stream
 };
 constexpr int kList = 64;                           // two batches of a warp
 
-// Ten warps with one stage each hide the math better than four with three, but
-// cut the slots into more ranges, whose lengths differ by one. Measured (32/8
-// heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120 slots 66.3 /
-// 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten slots a
-// range on.
+// A cluster of kCtas CTAs of kWarps warps with one stage each has one item: twelve
+// warps an SM (their rings are its shared memory).
+constexpr int kSmWarps = 12;
+// Without clusters the slots of all items are one line, cut into a range for each
+// warp of the device. Ten warps an SM with one stage each hide the math better than
+// four with three, but cut the slots into more ranges, whose lengths differ by one.
+// Measured (32/8 heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120
+// slots 66.3 / 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten
+// slots a range on.
 constexpr int kManyWarps = 10, kFewWarps = 4;
 constexpr int kManySlots = 10;
 
-// Few items: a cluster of eight CTAs for each (three CTAs fit an SM), where their
-// warps have at most one slot each and all clusters are resident together. Clusters
-// stay within a GPC, so that not all places can be had: an eighth is left out.
-// Measured, cluster / ranges and combine (us, 8 KV heads): K = 16, one sequence 7.1 /
-// 8.6, five 8.9 / 10.3, six (48 items) 9.1 / 10.4, eight (more than fit) 15.8 / 11.4;
-// K = 31, one 7.4 / 8.3, six 9.9 / 11.8; K = 32, one 9.2 / 8.8, four 11.0 / 9.8. A
-// call from Python, where the second launch costs: 18.1 / 20.5.
-constexpr int kClusterCtas = 8;
-constexpr int kClusterWarps = kClusterCtas * kFewWarps, kClusterCtasPerSm = 3;
-
-// kWarps warps of one CTA per SM, kDepth ring stages each, and their shared memory.
+// kWarps warps of a CTA, kDepth ring stages each, and their shared memory.
 template <int kWarps, int kDepth>
 struct Shape {
     static constexpr uint32_t kOffList = kWarps * kDepth * kStageBytes;
@@ -113,7 +111,7 @@ struct Params {
     int nslot;              // partial slots per query head
     float* part_o;          // [N * Hq, nslot, D]
     float* part_ml;         // [N * Hq, nslot, 2]
-    __nv_bfloat16* o;       // [N, Hq, D]; lse [N, Hq] or null (kernel of one cluster an item)
+    __nv_bfloat16* o;       // [N, Hq, D]; lse [N, Hq] or null (clusters; else the combine writes them)
     float* lse;
     int* status;
 };
@@ -142,14 +140,18 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int cta) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 ld_cluster(uint32_t addr) {
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
     return x;
 }
 // Every thread of every CTA of the cluster; what they wrote before is visible behind it.
+template <int kCtas>
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (kCtas == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -234,11 +236,11 @@ __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b)
     b.inv_vs = 1.f / r.vs;
 }
 
-// kCluster = 1: the ranges of the whole device, whose partials go to the workspace.
+// kCluster = 0: the ranges of the whole device, whose partials go to the workspace.
 // Otherwise a cluster of kCluster CTAs for each item: its warps cut the item's K + 1
 // slots, and their partials meet in the cluster's shared memory.
 template <int kWarps, int kDepth, int kCluster>
-__global__ void __launch_bounds__(kWarps * 32, kCluster == 1 ? 1 : kClusterCtasPerSm)
+__global__ void __launch_bounds__(kWarps * 32, kCluster == 0 ? 1 : kSmWarps / kWarps)
 decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_k8, const __grid_constant__ CUtensorMap map_v8, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -246,9 +248,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     after_previous();
     constexpr int kRanges = kWarps * kCluster;      // of an item
-    const int cta = (int)blockIdx.x % kCluster;
-    const int range = kCluster == 1 ? warp * (int)gridDim.x + (int)blockIdx.x : warp * kCluster + cta;
-    if (kCluster == 1 && range >= p.ranges) return;
+    const int cta = (int)blockIdx.x % max(kCluster, 1);
+    const int range = kCluster == 0 ? warp * (int)gridDim.x + (int)blockIdx.x : warp * kCluster + cta;
+    if (kCluster == 0 && range >= p.ranges) return;
 
     uint8_t* ring = smem + warp * kDepth * kStageBytes;
     Block* list = reinterpret_cast<Block*>(smem + Shape<kWarps, kDepth>::kOffList) + warp * kList;
@@ -264,11 +266,17 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     __syncwarp();
 
     const int Kp1 = p.K + 1;
-    const long long v0 = kCluster == 1 ? 0 : (long long)(blockIdx.x / kCluster) * Kp1;
-    const long long v1 = v0 + (kCluster == 1 ? range_begin(range + 1, p.V, p.ranges) : range_begin(range + 1, Kp1, kRanges));
-    long long v = v0 + (kCluster == 1 ? range_begin(range, p.V, p.ranges) : range_begin(range, Kp1, kRanges));  // next slot to resolve
+    const int own_item = (int)(blockIdx.x / max(kCluster, 1));
+    long long v, v1;            // next slot to resolve, end of the range
+    if constexpr (kCluster == 0) {
+        v = range_begin(range, p.V, p.ranges);
+        v1 = range_begin(range + 1, p.V, p.ranges);
+    } else {
+        v = (long long)own_item * Kp1 + range_begin(range, Kp1, kRanges);
+        v1 = (long long)own_item * Kp1 + range_begin(range + 1, Kp1, kRanges);
+    }
     const int last_item = (int)((v1 - 1) / Kp1);
-    int cur_item = kCluster == 1 ? (int)(v / Kp1) : (int)(blockIdx.x / kCluster);
+    int cur_item = kCluster == 0 ? (int)(v / Kp1) : own_item;
 
     const int grp = lane >> 2, tig = lane & 3;     // mma fragment coordinates
     // ldmatrix: this lane's row within 16 keys; chunk c of that row is at lofs ^ (c << 4) (c even; the odd
@@ -498,44 +506,52 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         volatile int no_abort = 0;
         for (uint32_t k = done; k < issued; ++k) mbar_wait(&full[k % kDepth], (k / kDepth) & 1, &no_abort, nullptr);
     }
-    if constexpr (kCluster == 1) {
+    if constexpr (kCluster == 0) {
         if (started) write(cur_item++);
         for (; cur_item <= last_item; ++cur_item) write_empty(cur_item);
     } else {
         // the warp's partial into its ring, which is done with
-        static_assert(kRanges == 32 && kWarps * 32 == kD, "a lane for each partial, a thread for each dimension");
+        static_assert(kRanges <= 32, "a lane for each partial");
         float2* ml = reinterpret_cast<float2*>(smem + Shape<kWarps, kDepth>::kOffMl);
         if (started)
             write_to(ml + warp * 8, reinterpret_cast<float*>(ring), 1);
         else if (lane < p.G)
             ml[warp * 8 + lane] = make_float2(-INFINITY, 0.f);
-        cluster_sync();
+        cluster_sync<kCluster>();
         const int n = cur_item / p.Hkv, h = cur_item % p.Hkv;
-        for (int g = cta; g < p.G; g += kCluster) {
-            const uint32_t at = cluster_addr(smem_u32(ml + lane / kCluster * 8 + g), lane % kCluster);
-            const float wm = ld_cluster(at), wl = ld_cluster(at + 4);
-            float M = wm;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        // the halves of the heads' rows, two dimensions a lane, over all warps of the cluster
+        for (int u = warp * kCluster + cta; u < 2 * p.G; u += kRanges) {
+            const int g = u >> 1, d = (u & 1) * 64 + 2 * lane;
+            float wm = -INFINITY, wl = 0.f;
+            if (lane < kRanges) {
+                const float2 w = ld_cluster(cluster_addr(smem_u32(ml + lane / kCluster * 8 + g), lane % kCluster));
+                wm = w.x, wl = w.y;
+            }
+            const float M = warp_max(wm);
             const float f = wm == -INFINITY ? 0.f : exp2f(wm - M);
-            const unsigned full_parts = __ballot_sync(0xffffffffu, wm != -INFINITY);
-            float L = wm == -INFINITY ? 0.f : wl * f, acc = 0.f;
+            const unsigned some = __ballot_sync(0xffffffffu, wm != -INFINITY);
+            float L = wm == -INFINITY ? 0.f : wl * f;
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 8
             for (int i = 0; i < kRanges; ++i) {
                 // (an empty partial's place is read all the same, and not used)
-                const float x = ld_cluster(cluster_addr(smem_u32(smem + i / kCluster * kDepth * kStageBytes) + (g * kD + threadIdx.x) * 4,
-                                                        i % kCluster));
+                const float2 x = ld_cluster(cluster_addr(
+                    smem_u32(smem + i / kCluster * kDepth * kStageBytes) + (g * kD + d) * (int)sizeof(float), i % kCluster));
                 const float fi = __shfl_sync(0xffffffffu, f, i);
-                if (full_parts >> i & 1) acc = fmaf(x, fi, acc);
+                if (some >> i & 1) {
+                    acc.x = fmaf(x.x, fi, acc.x);
+                    acc.y = fmaf(x.y, fi, acc.y);
+                }
             }
             const bool none = M == -INFINITY;
             const long long row = (long long)n * p.Hq + h * p.G + g;
-            p.o[row * kD + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : acc / L);
-            if (p.lse != nullptr && threadIdx.x == 0) p.lse[row] = none ? M : (M + log2f(L)) * kLn2;
+            *reinterpret_cast<__nv_bfloat162*>(p.o + row * kD + d) =
+                none ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.x / L, acc.y / L);
+            if (p.lse != nullptr && d == 0) p.lse[row] = none ? M : (M + log2f(L)) * kLn2;
         }
-        cluster_sync();             // nobody leaves while its partials are read
+        cluster_sync<kCluster>();   // nobody leaves while its partials are read
     }
 }
 
@@ -612,28 +628,60 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
 
 struct Layout {
     long long V;
-    bool many, cluster;
+    int warps, ctas;            // of a cluster; ctas 0: ranges
     int grid, ranges, nslot;
 };
+constexpr struct {
+    int warps, ctas;
+} kClusters[] = {{4, 8}, {3, 8}, {4, 4}, {3, 4}, {4, 2}, {3, 2}, {4, 1}, {3, 1}};        // most warps first
+
+// The clusters that go through their items' slots in the fewest rounds (of one slot a
+// warp): as many warps as still have all clusters resident together, or, with single
+// CTAs, waves of which the last is at least half full. (Clusters stay within a GPC, so
+// that not all places can be had: an eighth is left out.) Where one round does, the
+// fewest warps; else the most. Left to the ranges: few items with many slots (the
+// clusters' warps would be under half of what the device holds), and odd waves.
+// Measured (us, 8 KV heads, sequences x (K + 1): this choice / ranges and combine):
+// 1 x 17 6.9 / 8.6, 1 x 33 8.5 / 8.9 but 2 x 33 9.5 / 9.0 and 1 x 129 13.1 / 11.1,
+// 8 x 17 9.0 / 11.6, 4 x 33 10.7 / 9.8, 4 x 65 14.2 / 15.0, 8 x 33 13.3 / 15.9, 24 x 33
+// 25.0 / 27.9, 48 x 33 40.1 / 45.4, 64 x 33 50.7 / 55.6, 128 x 33 91.8 / 99.4, 8 x 1025
+// 164.8 / 171.2; with a last wave of a third: 72 x 33 66.1 / 60.0.
+void choose_clusters(Layout& r, long long items, int slots, int sms) {
+    r.ctas = 0;
+    long long best = 0;
+    for (const auto& c : kClusters) {
+        const long long most = (long long)(kSmWarps / c.warps) * sms * (c.ctas > 1 ? 7 : 8) / 8, need = items * c.ctas;
+        const long long waves = (need + most - 1) / most;
+        if (waves > 1 && (c.ctas > 1 || 2 * (need - (waves - 1) * most) < most)) continue;
+        const int warps = c.warps * c.ctas;
+        const long long rounds = waves * ((slots + warps - 1) / warps);
+        if (r.ctas && (rounds > best || (rounds == best && best > 1))) continue;
+        best = rounds;
+        r.warps = c.warps;
+        r.ctas = c.ctas;
+    }
+    if (best > 1 && 2 * items * kClusters[0].warps * kClusters[0].ctas < (long long)kSmWarps * sms) r.ctas = 0;
+    if (r.ctas) r.grid = (int)(items * r.ctas);
+}
+
 Layout layout(int N, int Hkv, int K) {
     Layout r;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
     r.V = (long long)N * Hkv * (K + 1);
-    r.many = r.V >= (long long)kManySlots * kManyWarps * sms;
+    r.warps = r.V >= (long long)kManySlots * kManyWarps * sms ? kManyWarps : kFewWarps;
     r.grid = (int)(r.V < sms ? r.V : sms);
-    const long long most = (long long)sms * (r.many ? kManyWarps : kFewWarps);
+    const long long most = (long long)sms * r.warps;
     r.ranges = (int)(r.V < most ? r.V : most);
     const long long mn = r.V / r.ranges;                     // shortest range
     const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
     r.nslot = (int)(span < r.ranges ? span : r.ranges);
-    r.cluster = K + 1 <= kClusterWarps && (long long)N * Hkv * kClusterCtas <= kClusterCtasPerSm * sms * 7 / 8;
-    if (r.cluster) r.grid = N * Hkv * kClusterCtas;
+    choose_clusters(r, (long long)N * Hkv, K + 1, sms);
     return r;
 }
 
-template <int kWarps, int kDepth, int kCluster = 1>
+template <int kWarps, int kDepth, int kCluster = 0>
 cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params& p, cudaStream_t st) {
     constexpr int kSmem = (int)Shape<kWarps, kDepth>::kSmem;
     const auto kernel = decode_q8_kernel<kWarps, kDepth, kCluster>;
@@ -646,6 +694,7 @@ cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params&
 
 size_t decode_q8_workspace(int N, int Hq, int Hkv, int K) {
     const Layout lay = layout(N, Hkv, K);
+    if (lay.ctas) return 256;       // none
     const size_t per = (size_t)N * Hq * lay.nslot;
     return sizeof(float) * (per * kD + per * 2);
 }
@@ -685,12 +734,22 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
     p.o = (__nv_bfloat16*)a.o;
     p.lse = a.lse;
     p.status = a.status;
-    if (lay.cluster) {
-        const cudaError_t e = launch<kFewWarps, 1, kClusterCtas>(lay, map, p, st);
+    cudaError_t e;
+    if (lay.ctas) {
+        if (lay.warps == 4)
+            e = lay.ctas == 8   ? launch<4, 1, 8>(lay, map, p, st)
+                : lay.ctas == 4 ? launch<4, 1, 4>(lay, map, p, st)
+                : lay.ctas == 2 ? launch<4, 1, 2>(lay, map, p, st)
+                                : launch<4, 1, 1>(lay, map, p, st);
+        else
+            e = lay.ctas == 8   ? launch<3, 1, 8>(lay, map, p, st)
+                : lay.ctas == 4 ? launch<3, 1, 4>(lay, map, p, st)
+                : lay.ctas == 2 ? launch<3, 1, 2>(lay, map, p, st)
+                                : launch<3, 1, 1>(lay, map, p, st);
         if (e == cudaSuccess) count_launches(1);
         return e;
     }
-    cudaError_t e = lay.many ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
+    e = lay.warps == kManyWarps ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
     if (e != cudaSuccess) return e;
     count_launches(1);
     e = launch_dependent(lay.nslot > 8 ? decode_q8_combine_kernel<4> : decode_q8_combine_kernel<1>, dim3((unsigned)(a.N * a.Hq)),
