@@ -3,10 +3,11 @@
 // launched this way calls after_previous() before it touches memory, which
 // waits until that kernel has finished and its writes are visible: only the
 // placement of the CTAs comes early. In a stream of calls this saves one to two
-// microseconds a kernel (a ragged append 20.5 -> 18.5 us). kEarly = false is for
-// persistent grids of several CTAs an SM: early CTAs only get the room that the
-// kernel in front leaves (norm + rotation of 8k tokens, captured: 30.3 us, early
-// 31.7; an 8k prompt appended behind a kernel of many small CTAs 41.1, early 55.4).
+// microseconds a kernel (a ragged append 20.5 -> 18.5 us). Early CTAs go
+// where the kernel in front leaves room first: a persistent grid of several CTAs an
+// SM needs shared memory that lets no more of them onto an SM (norm + rotation of 8k
+// tokens: 30.5 us, without 32.5). kEarly = false is for grids that lose all the same
+// (the append of an 8k prompt behind a kernel of many small CTAs: 41.1, early 55.4).
 #pragma once
 
 #include <cuda_runtime.h>

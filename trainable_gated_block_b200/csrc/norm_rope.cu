@@ -39,7 +39,11 @@ struct Fwd {
     static constexpr int kThreads = 128, kCtas = sizeof(T) == 2 ? 4 : 6, kStages = 2, kHeads = sizeof(T) == 2 ? 4 : 1;
     static constexpr int kSlots = kThreads / HeadRow<D>::kLanes;
     static constexpr int kPieces = kHeads * 2 * Raw8<T>::kPieces;      // 16-byte pieces of a thread and unit
-    static constexpr int kSmem = kStages * kPieces * kThreads * 16;
+    // so much that one more would not fit: CTAs that are placed while the kernel in front
+    // still runs must not crowd on the SMs that are free first (8k tokens, one call after
+    // the other: 30.5 us, without 32.5, without early launch 32.6)
+    static constexpr int kSmem = 227 * 1024 / (kCtas + 1) / 16 * 16;
+    static_assert(kSmem >= kStages * kPieces * kThreads * 16, "the ring");
 };
 template <typename T, int D>
 struct Bwd {
@@ -283,7 +287,7 @@ cudaError_t fwd(const NormRopeArgs& a, void* q_out, void* k_out, cudaStream_t st
     const uint32_t n = (uint32_t)a.T * (parts_of(a.Hq, S::kHeads) + parts_of(a.Hkv, S::kHeads));
     cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent<false>(norm_rope_kernel<T, D>, dim3(grid_for(n, S::kSlots, S::kCtas)), S::kThreads, S::kSmem, st, a, n,
+    e = launch_dependent(norm_rope_kernel<T, D>, dim3(grid_for(n, S::kSlots, S::kCtas)), S::kThreads, S::kSmem, st, a, n,
                                 static_cast<T*>(q_out), static_cast<T*>(k_out));
     if (e == cudaSuccess) count_launches(1);
     return e;
