@@ -103,6 +103,10 @@ __device__ __forceinline__ float row_max(const Row& x, float m) {
     }
     return m;
 }
+// Largest of the warp's magnitudes: without a sign the bits order like the values.
+__device__ __forceinline__ float warp_max_abs(float m) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
 // An infinity has no code: it is kept as NaN.
 __device__ __forceinline__ void drop_infinities(Half& x) {
 #pragma unroll
@@ -307,11 +311,11 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u) {
 
     PageScale ps{true, true, 1.f};
     if constexpr (kQ8) {
-        float m = warp_max(row_max(x, 0.f));        // (behind the shuffles every lane has read the old scale)
+        float m = warp_max_abs(row_max(x, 0.f));        // (behind the shuffles every lane has read the old scale)
         if (m == INFINITY) {
             drop_infinities(x.a);
             drop_infinities(x.b);
-            m = warp_max(row_max(x, 0.f));
+            m = warp_max_abs(row_max(x, 0.f));
         }
         ps = page_scale(t.lo, old, m);
         if (!ps.ok) {
@@ -662,16 +666,13 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
         auto block_max = [&] {
 #pragma unroll
             for (int i = 0; i < B::kKvHeads; ++i) {
-                const float r = warp_max(fresh ? row_max(y[i], 0.f) : 0.f);
+                const float r = warp_max_abs(fresh ? row_max(y[i], 0.f) : 0.f);
                 if ((threadIdx.x & 31) == 0) wmax[buf][i][threadIdx.x >> 5] = r;
             }
             __syncthreads();        // (and every thread has read the old scales, and its rows of this stage)
 #pragma unroll
             for (int i = 0; i < B::kKvHeads; ++i) {
-                float r = wmax[buf][i][(threadIdx.x & 31) % B::kWarps];
-#pragma unroll
-                for (int o = B::kWarps / 2; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
-                m[i] = r;
+                m[i] = warp_max_abs(wmax[buf][i][(threadIdx.x & 31) % B::kWarps]);
             }
             buf ^= 1;               // the next maxima go elsewhere: these may still be read
         };
