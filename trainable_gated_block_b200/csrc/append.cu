@@ -20,12 +20,12 @@
 // Each thread prefetches its pieces of the next unit with cp.async.
 //
 // Measured on one B200 (32/8 heads of 128): one token of one sequence 3.4 us, of 64
-// sequences into 8-bit pages 4.9, two of which fill a page, of 256 sequences 6.7
+// sequences into 8-bit pages 4.7, two of which fill a page, of 256 sequences 6.6
 // (22.5 with a CTA for each row; 6.9 and 8.8 where the filled pages' rows met in
 // shared memory instead of by shuffles, without their loads in flight together);
-// prompts of 8k and 32k tokens into bf16 pages 36.5 and 127.5 us (87 and 100% of the
+// prompts of 8k and 32k tokens into bf16 pages 36.7 and 127.5 us (87 and 100% of the
 // copy rate; as 64-row tiles of one head 42.5 and 147; 41 and 141 with the pages'
-// mean keys), into 8-bit pages 41.4 and 153 (70 and 76%): the blocks' barrier leaves
+// mean keys), into 8-bit pages 40.7 and 151 (72 and 78%): the blocks' barrier leaves
 // the latencies of one CTA's 16 warps in a row. (Reading the rows twice instead of
 // holding them in registers, for two or three CTAs an SM: 46.8 and 75 us at 8k.)
 #include <cuda_fp16.h>

