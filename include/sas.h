@@ -352,7 +352,8 @@ sas_status sas_decode_paged_noalloc(const void *q, const void *k_cache, const vo
                                     const float *log_gate, float sm_scale, void *o, float *lse,
                                     void *stream);
 
-/* Bytes of device workspace sas_decode_paged_q8 needs (0 on a bad argument). */
+/* Bytes of device workspace sas_decode_paged_q8 needs (0 on a bad argument; 256 where it
+ * keeps nothing there). */
 size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
 
 /*

@@ -286,10 +286,13 @@ def test_offsets_past_32_bits():
     _check(out, _ref(x))
 
 
-def test_repeats_streams_and_graphs():
-    """The same bits every time: on another stream, and from two captured graphs that share a workspace."""
-    x = {k: v.cuda() for k, v in _make([64 * 9 + 3, 300, 0, 64 * 20], 8, 2, 6, seed=13).items()}
-    ws = torch.empty(sas.decode_q8_workspace_bytes(4, 8, 2, D, 6), dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("K,none", [(6, True), (40, False)])
+def test_repeats_streams_and_graphs(K, none):
+    """The same bits every time: on another stream, and from two captured graphs that share a workspace (which
+    few block slots do not use)."""
+    x = {k: v.cuda() for k, v in _make([64 * 9 + 3, 300, 0, 64 * 50], 8, 2, K, seed=13).items()}
+    ws = torch.empty(sas.decode_q8_workspace_bytes(4, 8, 2, D, K), dtype=torch.uint8, device="cuda")
+    assert (ws.numel() == 256) == none
     first = sas.decode_paged_q8(**x, workspace=ws)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

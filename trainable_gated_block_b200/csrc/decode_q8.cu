@@ -703,7 +703,7 @@ cudaError_t launch(const Layout& lay, const CUtensorMap (&map)[4], const Params&
 
 size_t decode_q8_workspace(int N, int Hq, int Hkv, int K) {
     const Layout lay = layout(N, Hkv, K);
-    if (lay.ctas) return 256;       // none
+    if (lay.ctas) return 256;       // nothing is kept there (ranges need more: 520 bytes for one partial)
     const size_t per = (size_t)N * Hq * lay.nslot;
     return sizeof(float) * (per * kD + per * 2);
 }

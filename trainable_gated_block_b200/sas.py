@@ -406,6 +406,15 @@ def _workspace_bytes(call: str, dev: int, *sizes) -> int:
     return int(getattr(lib(), call)(*sizes))
 
 
+_NO_WORKSPACE = 256         # a size that stands for none (the C calls want an address all the same)
+
+
+@functools.lru_cache(maxsize=None)
+def _placeholder(dev: int):
+    """What stands in for a workspace that nothing is kept in."""
+    return torch.empty(_NO_WORKSPACE, dtype=torch.uint8, device=f"cuda:{dev}")
+
+
 def _dense_like(t):
     """An uninitialised contiguous tensor of t's shape, dtype and device (the cheapest way torch has)."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -445,6 +454,8 @@ def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, i
     if N == 0:
         return o, lse
     need = _workspace_bytes("sas_decode_q8_workspace_size", dev, N, Hq, Hkv, D, K)
+    if workspace is None and need == _NO_WORKSPACE:
+        workspace = _placeholder(dev)
     ws, ws_bytes, workspace = _workspace(workspace, need, dev, q)
     code = lib().sas_decode_paged_q8(*ptrs, P, pt, max_pages, kv, N, Hq, Hkv, D, page_size, K, *sel, sm_scale, o.data_ptr(),
                                  lse.data_ptr() if with_lse else None, ws, ws_bytes, _raw_stream(dev))
