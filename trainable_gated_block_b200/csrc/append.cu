@@ -15,19 +15,20 @@
 // head) of K or of V. Prompts are bound by HBM. Into bf16 pages, persistent CTAs take
 // units of four heads of one token of q, k or v, which share the token's angles.
 // Into 8-bit pages a scale needs all new rows of a page: there the units of k and v
-// of one (sequence, block, pair of heads) go to one CTA, so that new rows are read
-// and written once, their amax needs no second pass and no two CTAs share a scale.
+// of one (sequence, block, two heads of k or four of v) go to one CTA, so that new rows
+// are read and written once, their amax needs no second pass and no two CTAs share a scale.
 // Each thread prefetches its pieces of the next unit with cp.async.
 //
 // Measured on one B200 (32/8 heads of 128): one token of one sequence 3.4 us, of 64
-// sequences into 8-bit pages 4.7, two of which fill a page, of 256 sequences 6.6
+// sequences into 8-bit pages 4.0, two of which fill a page, of 256 sequences 5.8
 // (22.5 with a CTA for each row; 6.9 and 8.8 where the filled pages' rows met in
 // shared memory instead of by shuffles, without their loads in flight together);
 // prompts of 8k and 32k tokens into bf16 pages 36.7 and 127.5 us (87 and 100% of the
-// copy rate; as 64-row tiles of one head 42.5 and 147; 41 and 141 with the pages'
-// mean keys), into 8-bit pages 40.7 and 151 (72 and 78%): the blocks' barrier leaves
-// the latencies of one CTA's 16 warps in a row. (Reading the rows twice instead of
-// holding them in registers, for two or three CTAs an SM: 46.8 and 75 us at 8k.)
+// copy rate; as 64-row tiles of one head 42.5 and 147; 42 and 142 with the pages'
+// mean keys), into 8-bit pages 40.2 and 144 (73 and 81%; 44.5 and 160 with mean keys):
+// the blocks' barrier leaves the latencies of one CTA's 16 warps in a row. (Reading the
+// rows twice instead of holding them in registers, for two or three CTAs an SM: 46.8
+// and 75 us at 8k.)
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -142,11 +143,15 @@ __device__ __forceinline__ PageScale page_scale(int lo, float old, float m) {
     return p;
 }
 
-// The mean key of a filled page is summed in one order by all kernels: for each
-// warp w of kSlots row slots the rows slot and slot + kSlots of its slots, these over
-// the warp's slots (sum_slots), and the sums by w.
-constexpr int kSlots = 32;                  // row slots of a page: each has kPageRows / kSlots rows
-constexpr int kSlotRows = kPageRows / kSlots;
+// The mean key of a filled page is summed in one order by all kernels. A warp's row
+// slots take kPerWarp neighbouring rows a round, kRounds rounds a page. For each slot
+// the rounds of each of four groups are added, these sums by group, and the results
+// over the slots (sum_slots).
+constexpr int kGroups = 4;
+template <int D>
+struct Rounds {
+    static constexpr int kPerWarp = HeadRow<D>::kPerWarp, kRounds = kPageRows / kPerWarp, kOfGroup = kRounds / kGroups;
+};
 
 // Sums of a row over the warp's row slots. Each step halves what a lane keeps: it
 // ends with kKept pairs of neighbouring dimensions, from sum_dim on.
@@ -185,59 +190,53 @@ __device__ __forceinline__ SlotSum<D> sum_slots(int lane, const Row& r) {
 template <int D, bool kQ8>
 __device__ __forceinline__ void page_rows(const AppendArgs& a, bool is_v, int page, int h, int rows, int grown, float ratio,
                                           float unit, bool pool) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp, kRounds = kSlots / kPerWarp;
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = Rounds<D>::kPerWarp, kAt = Rounds<D>::kOfGroup;
     const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
     const long long head = (long long)page * a.Hkv + h, tile0 = head * kPageRows;
-    SlotSum<D> mean{};
-    // the loads of four rounds are in flight together
-    constexpr int kAt = 4;
+    Row sum{};
+    // two groups of rounds at a time: their loads are in flight together
 #pragma unroll 1
-    for (int k0 = 0; k0 < kRounds; k0 += kAt) {
+    for (int g0 = 0; g0 < kGroups; g0 += 2) {
         using Piece = typename std::conditional<kQ8, uint2, uint4>::type;
-        Piece c[kAt][kSlotRows][2];
-        auto at = [&](int k, int i) { return kSlots * i + kPerWarp * (k0 + k) + grp; };
+        Piece c[2 * kAt][2];
         auto ptr = [&](int r) {
             return static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ((tile0 + r) * D + 8 * l) * (kQ8 ? 1 : 2);
         };
         constexpr int kHalf = D / 2 * (kQ8 ? 1 : 2);            // bytes
 #pragma unroll
-        for (int k = 0; k < kAt; ++k)
-#pragma unroll
-            for (int i = 0; i < kSlotRows; ++i) {
-                const int r = at(k, i);
-                c[k][i][0] = c[k][i][1] = Piece{};
-                if (r < rows) {
-                    c[k][i][0] = *reinterpret_cast<const Piece*>(ptr(r));
-                    c[k][i][1] = *reinterpret_cast<const Piece*>(ptr(r) + kHalf);
-                }
+        for (int k = 0; k < 2 * kAt; ++k) {
+            const int r = (g0 * kAt + k) * kPerWarp + grp;
+            c[k][0] = c[k][1] = Piece{};
+            if (r < rows) {
+                c[k][0] = *reinterpret_cast<const Piece*>(ptr(r));
+                c[k][1] = *reinterpret_cast<const Piece*>(ptr(r) + kHalf);
             }
+        }
 #pragma unroll
-        for (int k = 0; k < kAt; ++k) {
-            Row row[kSlotRows];
+        for (int g = 0; g < 2; ++g) {
+            Row group{};
 #pragma unroll
-            for (int i = 0; i < kSlotRows; ++i) {
+            for (int k = g * kAt; k < (g + 1) * kAt; ++k) {
                 if constexpr (kQ8) {
-                    const int r = at(k, i);
+                    const int r = (g0 * kAt + k) * kPerWarp + grp;
                     if (r < grown) {
-                        *reinterpret_cast<uint2*>(ptr(r)) = c[k][i][0] = to_codes(from_codes(c[k][i][0]), ratio);
-                        *reinterpret_cast<uint2*>(ptr(r) + kHalf) = c[k][i][1] = to_codes(from_codes(c[k][i][1]), ratio);
+                        *reinterpret_cast<uint2*>(ptr(r)) = c[k][0] = to_codes(from_codes(c[k][0]), ratio);
+                        *reinterpret_cast<uint2*>(ptr(r) + kHalf) = c[k][1] = to_codes(from_codes(c[k][1]), ratio);
                     }
-                    row[i] = {from_codes(c[k][i][0]), from_codes(c[k][i][1])};
+                    add(group.a, from_codes(c[k][0]));
+                    add(group.b, from_codes(c[k][1]));
                 } else {
-                    const uint4 lo[1] = {c[k][i][0]}, hi[1] = {c[k][i][1]};
-                    row[i] = {Raw8<bf16>::get(lo), Raw8<bf16>::get(hi)};
+                    const uint4 lo[1] = {c[k][0]}, hi[1] = {c[k][1]};
+                    add(group.a, Raw8<bf16>::get(lo));
+                    add(group.b, Raw8<bf16>::get(hi));
                 }
             }
-            if (!pool) continue;
-            static_assert(kSlotRows == 2, "rows of a slot");
-            add(row[0].a, row[1].a);
-            add(row[0].b, row[1].b);
-            const SlotSum<D> s = sum_slots<D>(lane, row[0]);
-#pragma unroll
-            for (int i = 0; i < SlotSum<D>::kKept; ++i) mean.v[i] = f2_add(mean.v[i], s.v[i]);
+            add(sum.a, group.a);
+            add(sum.b, group.b);
         }
     }
     if (!pool) return;
+    const SlotSum<D> mean = sum_slots<D>(lane, sum);
     const f2 u = f2_pack(unit, unit), n = f2_pack(1.f / kPageRows, 1.f / kPageRows);
     f2* out = reinterpret_cast<f2*>(a.kpool + head * D + sum_dim<D>(lane));
 #pragma unroll
@@ -414,14 +413,14 @@ struct Unit {
     int kind, t, part, pos, page;
 };
 // Starts the copies of a unit (row pieces of kThreads threads each) into a stage.
-template <int D, int kThreads, int kKvHeads>
+template <int D, int kThreads, int kKHeads, int kVHeads>
 __device__ __forceinline__ void issue(const AppendArgs& a, const Unit& r, uint32_t at) {
     const int l = threadIdx.x % HeadRow<D>::kLanes;
     if (r.kind != kNone) {
         const bf16* src = r.kind == kQ   ? static_cast<const bf16*>(a.q) + r.t * a.ld_q
                           : r.kind == kK ? static_cast<const bf16*>(a.k) + r.t * a.ld_k
                                          : static_cast<const bf16*>(a.v) + r.t * a.ld_v;
-        const int H = r.kind == kQ ? a.Hq : a.Hkv, heads = r.kind == kQ ? kHeads : kKvHeads, parts = (int)parts_of(H, heads);
+        const int H = r.kind == kQ ? a.Hq : a.Hkv, heads = r.kind == kQ ? kHeads : r.kind == kK ? kKHeads : kVHeads, parts = (int)parts_of(H, heads);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
             if (i >= heads) break;
@@ -462,11 +461,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
         return r;
     };
     Unit cur = unit_at(first);
-    issue<D, kThreads, kHeads>(a, cur, ring);
+    issue<D, kThreads, kHeads, kHeads>(a, cur, ring);
     uint32_t st = 0;
     for (uint32_t base = blockIdx.x * kCtaSlots, u = first; base < units; base += step, u += step) {
         const Unit next = unit_at(u + step);
-        issue<D, kThreads, kHeads>(a, next, ring + (st ^ 1) * kStageBytes);
+        issue<D, kThreads, kHeads, kHeads>(a, next, ring + (st ^ 1) * kStageBytes);
         const bool is_q = cur.kind == kQ, is_v = cur.kind == kV;
         const bf16* weight = static_cast<const bf16*>(is_q ? a.q_weight : a.k_weight);
         const Turn turn(load_angles<bf16, D>(a.table, cur.pos, l), load_weight<bf16, D>(weight, l));
@@ -509,43 +508,45 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rows_kernel(const Appe
 // tile's loads are all in flight together.
 template <int D>
 __global__ void __launch_bounds__(kThreads) pool_filled_kernel(const AppendArgs a) {
-    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = HeadRow<D>::kPerWarp, kRounds = kSlots / kPerWarp;
-    constexpr int kOfWarp = kRounds / (kThreads / 32);
-    __shared__ __align__(16) float red[kRounds][D];
+    constexpr int kLanes = HeadRow<D>::kLanes, kPerWarp = Rounds<D>::kPerWarp, kAt = Rounds<D>::kOfGroup;
+    static_assert(kThreads / 32 == kGroups, "a warp for each group of rounds");
+    __shared__ __align__(16) float red[kGroups][kPerWarp][D];
     after_previous();
     SeqAt seq;
     const PageTile t = seq.find_tile(a, blockIdx.x / a.Hkv);
     if (t.hi != kPageRows || t.hi <= t.lo) return;
     const int page = seq.page(a, t.block);
     if (page < 0 || page >= a.num_pages) return;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, first = threadIdx.x / 32 * kOfWarp;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes, warp = threadIdx.x / 32;
     const long long head = (long long)page * a.Hkv + blockIdx.x % a.Hkv;
-    const bf16* rows = static_cast<const bf16*>(a.k_cache) + (head * kPageRows + first * kPerWarp + lane / kLanes) * D + 8 * l;
-    uint4 c[kOfWarp][kSlotRows][2][1];
+    const bf16* rows = static_cast<const bf16*>(a.k_cache) + (head * kPageRows + warp * kAt * kPerWarp + grp) * D + 8 * l;
+    uint4 c[kAt][2][1];
 #pragma unroll
-    for (int k = 0; k < kOfWarp; ++k)
-#pragma unroll
-        for (int i = 0; i < kSlotRows; ++i) {
-            const bf16* row = rows + (k * kPerWarp + i * kSlots) * D;
-            c[k][i][0][0] = *reinterpret_cast<const uint4*>(row);
-            c[k][i][1][0] = *reinterpret_cast<const uint4*>(row + D / 2);
-        }
-#pragma unroll
-    for (int k = 0; k < kOfWarp; ++k) {
-        Row r = {Raw8<bf16>::get(c[k][0][0]), Raw8<bf16>::get(c[k][0][1])};
-        add(r.a, Raw8<bf16>::get(c[k][1][0]));
-        add(r.b, Raw8<bf16>::get(c[k][1][1]));
-        const SlotSum<D> s = sum_slots<D>(lane, r);
-        f2* to = reinterpret_cast<f2*>(&red[first + k][sum_dim<D>(lane)]);
-#pragma unroll
-        for (int i = 0; i < SlotSum<D>::kKept; ++i) to[i] = s.v[i];
+    for (int k = 0; k < kAt; ++k) {
+        c[k][0][0] = *reinterpret_cast<const uint4*>(rows + k * kPerWarp * D);
+        c[k][1][0] = *reinterpret_cast<const uint4*>(rows + k * kPerWarp * D + D / 2);
     }
+    Row group{};
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+        add(group.a, Raw8<bf16>::get(c[k][0]));
+        add(group.b, Raw8<bf16>::get(c[k][1]));
+    }
+    store_sum<D>(red[warp][grp], l, group);
     __syncthreads();
     if (threadIdx.x >= D) return;
-    float total = 0.f;
+    float part[kPerWarp];
 #pragma unroll
-    for (int k = 0; k < kRounds; ++k) total += red[k][threadIdx.x];
-    a.kpool[head * D + threadIdx.x] = total * (1.f / kPageRows);
+    for (int r = 0; r < kPerWarp; ++r) {
+        part[r] = 0.f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) part[r] += red[g][r][threadIdx.x];
+    }
+#pragma unroll
+    for (int n = 1; n < kPerWarp; n *= 2)
+#pragma unroll
+        for (int r = 0; r < kPerWarp; r += 2 * n) part[r] += part[r + n];
+    a.kpool[head * D + threadIdx.x] = part[0] * (1.f / kPageRows);
 }
 
 // ------------------------------------------------------------------ prompts into 8-bit pages
@@ -556,20 +557,28 @@ template <int D>
 struct Blocks {
     static constexpr int kThreads = kPageRows * HeadRow<D>::kLanes, kCtas = 512 / kThreads;     // CTAs of an SM
     static constexpr int kWarps = kThreads / 32;
-    static constexpr int kKvHeads = 2;       // heads of a unit of keys or values (four would not fit the registers)
+    // heads of a work: as many as the registers hold between the largest magnitude and the
+    // codes (keys: with their rotation. V of two heads: 40.7 and 151 us at 8k and 32k
+    // instead of 40.2 and 144; K of four: spills, 46.0 and 163)
+    static constexpr int kKHeads = 2, kVHeads = 4;
     static constexpr int kStageBytes = 2 * kHeads * kThreads * 16;
-    static constexpr int kSmem = kStages * kStageBytes;
+    static constexpr int kRing = kStages * kStageBytes;
+    // fp32 rows of a page and the work's heads of keys, for their mean; padded so that a
+    // warp's row slots meet no bank twice
+    static constexpr int kStride = D + 32 / HeadRow<D>::kPerWarp;
+    static constexpr int kRed = kKHeads * kPageRows * kStride * 4;
 };
 template <int D>
 __global__ void __launch_bounds__(Blocks<D>::kThreads, Blocks<D>::kCtas)
 append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, uint32_t works) {
     using B = Blocks<D>;
     extern __shared__ __align__(16) uint8_t ring_s[];
-    __shared__ float wmax[2][B::kKvHeads][B::kWarps];
+    __shared__ float wmax[2][B::kVHeads][B::kWarps];
     after_previous();
     const uint32_t ring = sm100::smem_u32(ring_s) + threadIdx.x * 16;
+    float(*red)[kPageRows][B::kStride] = reinterpret_cast<float(*)[kPageRows][B::kStride]>(ring_s + B::kRing);   // with kpool
     const int l = threadIdx.x % HeadRow<D>::kLanes, slot = threadIdx.x / HeadRow<D>::kLanes;
-    const int q_parts = (int)parts_of(a.Hq, kHeads), kv_parts = (int)parts_of(a.Hkv, B::kKvHeads);
+    const int q_parts = (int)parts_of(a.Hq, kHeads), k_parts = (int)parts_of(a.Hkv, B::kKHeads), v_parts = (int)parts_of(a.Hkv, B::kVHeads);
 
     // the unit, and of a block of keys or values its rows lo .. hi - 1 that are new (all slots: `rows`, 0: none)
     struct Work {
@@ -588,12 +597,12 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
             k.u = {kQ, (int)t, (int)(u - t * q_parts), seq.first + (int)t - seq.row0, 0};
             return k;
         }
-        const uint32_t v = w / (2u * kv_parts), rest = w - v * 2u * kv_parts;
+        const uint32_t per = k_parts + v_parts, v = w / per, rest = w - v * per;
         const PageTile t = seq.find_tile(a, v);
         if (t.hi <= t.lo) return k;
         k.rows = t.lo | t.hi << 8;
-        const bool is_v = rest >= (uint32_t)kv_parts;
-        k.u.part = (int)(is_v ? rest - kv_parts : rest);
+        const bool is_v = rest >= (uint32_t)k_parts;
+        k.u.part = (int)(is_v ? rest - k_parts : rest);
         k.u.pos = t.block * kPageRows + slot;
         k.u.page = seq.page(a, t.block);
         k.u.t = (int)t.row + slot - t.lo;
@@ -604,7 +613,7 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
     auto issue_work = [&](const Work& k, uint32_t at) {
         Unit u = k.u;
         if (k.rows != 0 && (slot < k.lo() || slot >= k.hi())) u.kind = kNone;
-        issue<D, B::kThreads, B::kKvHeads>(a, u, at);
+        issue<D, B::kThreads, B::kKHeads, B::kVHeads>(a, u, at);
     };
     constexpr int kRow = 2 * B::kThreads * 16;
 
@@ -634,114 +643,126 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
             continue;
         }
         // keys or values (uniform over the CTA up to the slot's row)
-        const int lo = cur.lo(), hi = cur.hi();
-        const bool is_v = u.kind == kV, fresh = slot >= lo && slot < hi, page_ok = u.page >= 0 && u.page < a.num_pages;
-        if (!page_ok && threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-        bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
-        const long long head0 = (long long)(page_ok ? u.page : 0) * a.Hkv;
-        float* scale = (is_v ? a.v_scale : a.k_scale) + head0;
-        float old[B::kKvHeads];
+        auto block = [&](auto values) {
+            constexpr bool is_v = decltype(values)::value;
+            constexpr int kN = is_v ? B::kVHeads : B::kKHeads;
+            const int parts = is_v ? v_parts : k_parts;
+            const int lo = cur.lo(), hi = cur.hi();
+            const bool fresh = slot >= lo && slot < hi, page_ok = u.page >= 0 && u.page < a.num_pages;
+            if (!page_ok && threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+            bf16* k_out = is_v ? nullptr : static_cast<bf16*>(a.k_out);
+            const long long head0 = (long long)(page_ok ? u.page : 0) * a.Hkv;
+            float* scale = (is_v ? a.v_scale : a.k_scale) + head0;
+            float old[kN];
 #pragma unroll
-        for (int i = 0; i < B::kKvHeads; ++i) {
-            const int h = u.part + i * kv_parts;
-            old[i] = page_ok && lo > 0 && h < a.Hkv ? scale[h] : 0.f;
-        }
-        Row y[B::kKvHeads];
-        if (is_v) {
-#pragma unroll
-            for (int i = 0; i < B::kKvHeads; ++i) y[i] = read_row<bf16, B::kThreads>(at + i * kRow);
-        } else {
-            const bf16* weight = static_cast<const bf16*>(a.k_weight);
-            const int pos = min(max(u.pos, u.pos - slot + lo), u.pos - slot + hi - 1);
-            const Turn turn(load_angles<bf16, D>(a.table, pos, l), load_weight<bf16, D>(weight, l));
-#pragma unroll
-            for (int i = 0; i < B::kKvHeads; ++i) {
-                const int h = u.part + i * kv_parts;
-                const Row x = read_row<bf16, B::kThreads>(at + i * kRow);
-                y[i] = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
-                if (k_out != nullptr && fresh && h < a.Hkv) store_row<D>(k_out + ((long long)u.t * a.Hkv + h) * D, l, y[i]);
+            for (int i = 0; i < kN; ++i) {
+                const int h = u.part + i * parts;
+                old[i] = page_ok && lo > 0 && h < a.Hkv ? scale[h] : 0.f;
             }
-        }
-        float m[B::kKvHeads];
-        auto block_max = [&] {
+            Row y[kN];
+            if constexpr (is_v) {
 #pragma unroll
-            for (int i = 0; i < B::kKvHeads; ++i) {
-                const float r = warp_max_abs(fresh ? row_max(y[i], 0.f) : 0.f);
-                if ((threadIdx.x & 31) == 0) wmax[buf][i][threadIdx.x >> 5] = r;
-            }
-            __syncthreads();        // (and every thread has read the old scales, and its rows of this stage)
+                for (int i = 0; i < kN; ++i) y[i] = read_row<bf16, B::kThreads>(at + i * kRow);
+            } else {
+                const bf16* weight = static_cast<const bf16*>(a.k_weight);
+                const int pos = min(max(u.pos, u.pos - slot + lo), u.pos - slot + hi - 1);
+                const Turn turn(load_angles<bf16, D>(a.table, pos, l), load_weight<bf16, D>(weight, l));
 #pragma unroll
-            for (int i = 0; i < B::kKvHeads; ++i) {
-                m[i] = warp_max_abs(wmax[buf][i][(threadIdx.x & 31) % B::kWarps]);
-            }
-            buf ^= 1;               // the next maxima go elsewhere: these may still be read
-        };
-        block_max();
-        float top = m[0];
-#pragma unroll
-        for (int i = 1; i < B::kKvHeads; ++i) top = fmaxf(top, m[i]);
-        if (top == INFINITY) {
-#pragma unroll
-            for (int i = 0; i < B::kKvHeads; ++i) {
-                drop_infinities(y[i].a);
-                drop_infinities(y[i].b);
-            }
-            block_max();
-        }
-        const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows && page_ok;
-#pragma unroll
-        for (int i = 0; i < B::kKvHeads; ++i) {
-            const int h = u.part + i * kv_parts;
-            if (!page_ok || h >= a.Hkv) continue;
-            const PageScale ps = page_scale(lo, old[i], m[i]);
-            if (!ps.ok) {
-                if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
-                continue;
-            }
-            if (threadIdx.x == 0 && !ps.keep) scale[h] = ps.s;
-            uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ((head0 + h) * kPageRows + slot) * D + 8 * l;
-            uint2 c = make_uint2(0u, 0u), c2 = c;
-            if (fresh) {
-                c = to_codes(y[i].a, 1.f / ps.s);
-                c2 = to_codes(y[i].b, 1.f / ps.s);
-            } else if (slot < lo && (!ps.keep || pool)) {
-                c = *reinterpret_cast<const uint2*>(row);
-                c2 = *reinterpret_cast<const uint2*>(row + D / 2);
-                if (!ps.keep) {
-                    c = to_codes(from_codes(c), old[i] * (1.f / ps.s));
-                    c2 = to_codes(from_codes(c2), old[i] * (1.f / ps.s));
+                for (int i = 0; i < kN; ++i) {
+                    const int h = u.part + i * parts;
+                    const Row x = read_row<bf16, B::kThreads>(at + i * kRow);
+                    y[i] = turn(x, weight != nullptr ? row_rrms<D>(x, a.eps) : 1.f);
+                    if (k_out != nullptr && fresh && h < a.Hkv) store_row<D>(k_out + ((long long)u.t * a.Hkv + h) * D, l, y[i]);
                 }
             }
-            if (fresh || (slot < lo && !ps.keep)) {
-                *reinterpret_cast<uint2*>(row) = c;
-                *reinterpret_cast<uint2*>(row + D / 2) = c2;
+            float m[kN];
+            auto block_max = [&] {
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const float r = warp_max_abs(fresh ? row_max(y[i], 0.f) : 0.f);
+                    if ((threadIdx.x & 31) == 0) wmax[buf][i][threadIdx.x >> 5] = r;
+                }
+                __syncthreads();        // (and every thread has read the old scales, and its rows of this stage)
+#pragma unroll
+                for (int i = 0; i < kN; ++i) m[i] = warp_max_abs(wmax[buf][i][(threadIdx.x & 31) % B::kWarps]);
+                buf ^= 1;               // the next maxima go elsewhere: these may still be read
+            };
+            block_max();
+            float top = m[0];
+#pragma unroll
+            for (int i = 1; i < kN; ++i) top = fmaxf(top, m[i]);
+            if (top == INFINITY) {
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    drop_infinities(y[i].a);
+                    drop_infinities(y[i].b);
+                }
+                block_max();
+            }
+            const bool pool = a.kpool != nullptr && !is_v && hi == kPageRows && page_ok;
+            float unit[kN];             // scales of the heads whose mean key is wanted
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int h = u.part + i * parts;
+                unit[i] = 0.f;
+                if (!page_ok || h >= a.Hkv) continue;
+                const PageScale ps = page_scale(lo, old[i], m[i]);
+                if (!ps.ok) {
+                    if (threadIdx.x == 0) flag_status(a.status, kStatusBadData);
+                    continue;
+                }
+                if (threadIdx.x == 0 && !ps.keep) scale[h] = ps.s;
+                uint8_t* row = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + ((head0 + h) * kPageRows + slot) * D + 8 * l;
+                uint2 c = make_uint2(0u, 0u), c2 = c;
+                if (fresh) {
+                    c = to_codes(y[i].a, 1.f / ps.s);
+                    c2 = to_codes(y[i].b, 1.f / ps.s);
+                } else if (slot < lo && (!ps.keep || pool)) {
+                    c = *reinterpret_cast<const uint2*>(row);
+                    c2 = *reinterpret_cast<const uint2*>(row + D / 2);
+                    if (!ps.keep) {
+                        c = to_codes(from_codes(c), old[i] * (1.f / ps.s));
+                        c2 = to_codes(from_codes(c2), old[i] * (1.f / ps.s));
+                    }
+                }
+                if (fresh || (slot < lo && !ps.keep)) {
+                    *reinterpret_cast<uint2*>(row) = c;
+                    *reinterpret_cast<uint2*>(row + D / 2) = c2;
+                }
+                if (pool) {
+                    store_sum<D>(red[i][slot], l, Row{from_codes(c), from_codes(c2)});
+                    unit[i] = ps.s;
+                }
             }
             if (pool) {
-                // the mean key of the filled page, in the order of page_rows, where the stage's rows were
-                static_assert(kPageRows * D * 4 <= B::kStageBytes, "a head's rows in fp32");
-                constexpr int kPerWarp = HeadRow<D>::kPerWarp;
-                float(*red)[D] = reinterpret_cast<float(*)[D]>(ring_s + (st ^ 1) * B::kStageBytes);
-                store_sum<D>(red[slot], l, Row{from_codes(c), from_codes(c2)});
+                // the mean keys of the filled page, in the order of page_rows: a thread for each
+                // row slot of a warp and dimension. (The next block's maxima meet at a barrier
+                // before `red` is written again.)
+                constexpr int kPerWarp = Rounds<D>::kPerWarp, kAt = Rounds<D>::kOfGroup;
+                static_assert(B::kThreads % (kPerWarp * kPerWarp) == 0, "whole warps");
                 __syncthreads();
-                if (threadIdx.x < D) {
+#pragma unroll
+                for (int e = threadIdx.x; e < kN * kPerWarp * D; e += B::kThreads) {
+                    const int i = e / (kPerWarp * D), r = e % kPerWarp, d = e / kPerWarp % D;
                     float total = 0.f;
-#pragma unroll 2
-                    for (int g = 0; g < kSlots / kPerWarp; ++g) {
-                        float part[kPerWarp];
 #pragma unroll
-                        for (int r = 0; r < kPerWarp; ++r)
-                            part[r] = red[g * kPerWarp + r][threadIdx.x] + red[g * kPerWarp + r + kSlots][threadIdx.x];
+                    for (int g = 0; g < kGroups; ++g) {
+                        float group = 0.f;
 #pragma unroll
-                        for (int n = 1; n < kPerWarp; n *= 2)
-#pragma unroll
-                            for (int r = 0; r < kPerWarp; r += 2 * n) part[r] += part[r + n];
-                        total += part[0];
+                        for (int k = 0; k < kAt; ++k) group += red[i][(g * kAt + k) * kPerWarp + r][d];
+                        total += group;
                     }
-                    a.kpool[(head0 + h) * D + threadIdx.x] = total * ps.s * (1.f / kPageRows);
+#pragma unroll
+                    for (int n = 1; n < kPerWarp; n *= 2) total += __shfl_xor_sync(0xffffffffu, total, n);
+                    const float s = unit[i];
+                    if (r == 0 && s > 0.f) a.kpool[(head0 + u.part + i * parts) * D + d] = total * s * (1.f / kPageRows);
                 }
-                __syncthreads();    // read before the next head's rows, or the stage's next copies
             }
-        }
+        };
+        if (u.kind == kV)
+            block(std::true_type());
+        else
+            block(std::false_type());
         cur = next;
     }
     copy_wait<0>();
@@ -767,12 +788,13 @@ cudaError_t go(const AppendArgs& a, cudaStream_t st) {
     const long long q_parts = a.q != nullptr ? parts_of(a.Hq, kHeads) : 0;
     if constexpr (kQ8) {
         using B = Blocks<D>;
-        e = cudaFuncSetAttribute(append_blocks_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, B::kSmem);
+        const int smem = B::kRing + (a.kpool != nullptr ? B::kRed : 0);
+        e = cudaFuncSetAttribute(append_blocks_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, B::kRing + B::kRed);
         if (e != cudaSuccess) return e;
-        const long long kv_works = blocks * 2 * parts_of(a.Hkv, B::kKvHeads), q_units = a.T * q_parts;
+        const long long kv_works = blocks * (parts_of(a.Hkv, B::kKHeads) + parts_of(a.Hkv, B::kVHeads)), q_units = a.T * q_parts;
         const long long works = kv_works + (q_units + kPageRows - 1) / kPageRows;
         e = launch_dependent(append_blocks_kernel<D>, dim3((unsigned)std::min(works, (long long)B::kCtas * sms)), B::kThreads,
-                             B::kSmem, st, a, (uint32_t)kv_works, (uint32_t)q_units, (uint32_t)works);
+                             smem, st, a, (uint32_t)kv_works, (uint32_t)q_units, (uint32_t)works);
     } else {
         constexpr long long kCtaSlots = kThreads / HeadRow<D>::kLanes;
         const long long units = a.T * (q_parts + 2 * parts_of(a.Hkv, kHeads));
