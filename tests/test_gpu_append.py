@@ -179,6 +179,46 @@ def test_pieces_of_prompts(q8, D, Hq, Hkv, starts, news):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 6, 3), (128, 10, 5), (128, 6, 6), (128, 7, 7), (64, 9, 9), (64, 5, 1), (64, 3, 3)])
+def test_heads_that_do_not_fill_a_unit(q8, D, Hq, Hkv):
+    """Pieces that start and end inside pages, with counts of heads that leave a last unit part empty."""
+    starts, news = [20, 0, 63], [140, 64, 1]
+    P, pt = _layout(starts, news, seed=Hkv)
+    kv = torch.tensor([s + n for s, n in zip(starts, news)], dtype=torch.int32)
+    cu = torch.tensor([0] + news).cumsum(0).to(torch.int32)
+    tok, dev = _tokens(sum(news), Hq, Hkv, D, seed=Hq + D)
+    _check_call(Cache(q8, P, Hkv, D, seed=26), tok, dev, sas.rope_table(200, D), pt, kv, cu, max(news))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_mean_keys_by_prompt_and_by_token_have_the_same_bits(q8, D):
+    """Without rotation. In 8-bit pages of values on the codes' grid the sums are exact too."""
+    Hq = Hkv = 3
+    g = torch.Generator().manual_seed(27)
+    if q8:
+        k = torch.randint(-15, 16, (128, Hkv, D), generator=g).float()
+        k[::64] = 448.0                 # a page's first row sets its scale to 1
+    else:
+        k = torch.randn((128, Hkv, D), generator=g)
+    k = k.to(torch.bfloat16).cuda()
+    q = torch.zeros((128, Hq, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.cat((torch.ones((128, D // 2)), torch.zeros((128, D // 2))), dim=1).cuda()
+    pt = torch.tensor([[1, 0]], dtype=torch.int32).cuda()
+    a, b = Cache(q8, 2, Hkv, D, seed=28), Cache(q8, 2, Hkv, D, seed=28)
+    a.append(q, k, k, table, pt, torch.tensor([128], dtype=torch.int32).cuda(),
+             cu_new=torch.tensor([0, 128], dtype=torch.int32).cuda(), max_new=128)
+    for i in range(128):
+        b.append(q[i:i + 1], k[i:i + 1], k[i:i + 1], table, pt, torch.tensor([i + 1], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    sas.get_error_flag()
+    assert torch.equal(a.k.float(), b.k.float()) and torch.equal(a.kpool, b.kpool)
+    if q8:
+        assert torch.all(a.ks == 1.0) and torch.all(b.ks == 1.0)
+        assert torch.equal(a.kpool.double(), k.view(2, 64, Hkv, D).double().mean(1)[[1, 0]])    # page 1: the first block
+
+
+@pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 6, 3)])
 def test_single_tokens_of_some_sequences(q8, D, Hq, Hkv):
     """cu_new with max_new 1: sequences that bring a token and others that bring none."""
