@@ -141,6 +141,22 @@ def test_every_way_to_cut_the_work(Hq, Hkv, N, K):
     _check(_run(x), _ref(x))
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,K", [(3, 24, 8, 620), (1, 8, 8, 1900), (3, 16, 8, 300), (2, 2, 1, 700)])
+def test_few_items_with_many_slots(N, Hq, Hkv, K):
+    """Fewer than 28 items: the device's ranges, of ten warps an SM from 14,800 slots on and of four below.
+    The sequences share pages."""
+    x = _make([64 * 20] * N, Hq, Hkv, 0, seed=40)
+    g = torch.Generator().manual_seed(41)
+    P, blocks = x["k_cache"].shape[0], K + 40
+    x["page_table"] = torch.randint(0, P, (N, blocks + 1), generator=g, dtype=torch.int32)
+    x["kv_len"] = torch.tensor([64 * blocks + 9 + n for n in range(N)], dtype=torch.int32)
+    x["cnt"] = torch.full((N, Hkv), K, dtype=torch.int32)
+    x["idx"] = torch.stack([torch.randperm(blocks, generator=g)[:K].sort().values for _ in range(N * Hkv)])
+    x["idx"] = x["idx"].view(N, Hkv, K).to(torch.int32)
+    x["log_gate"] = -torch.rand((N, Hkv, K), generator=g) * 4
+    _check(_run(x), _ref(x))
+
+
 def test_all_history_of_a_long_sequence():
     x = _make([64 * 300 + 5], 8, 2, 300, seed=5)
     _check(_run(x, sm_scale=0.03), _ref(x, 0.03))

@@ -637,7 +637,8 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
 
 struct Layout {
     long long V;
-    int warps, ctas;            // of a cluster; ctas 0: ranges
+    int warps;                  // of a CTA
+    int ctas = 0;               // of a cluster; 0: ranges
     int grid, ranges, nslot;
 };
 constexpr struct {
@@ -655,8 +656,7 @@ constexpr struct {
 // 8 x 17 9.0 / 11.6, 4 x 33 10.7 / 9.8, 4 x 65 14.2 / 15.0, 8 x 33 13.3 / 15.9, 24 x 33
 // 25.0 / 27.9, 48 x 33 40.1 / 45.4, 64 x 33 50.7 / 55.6, 128 x 33 91.8 / 99.4, 8 x 1025
 // 164.8 / 171.2; with a last wave of a third: 72 x 33 66.1 / 60.0.
-void choose_clusters(Layout& r, long long items, int slots, int sms) {
-    r.ctas = 0;
+bool choose_clusters(long long items, int slots, int sms, int& cta_warps, int& ctas) {
     long long best = 0;
     for (const auto& c : kClusters) {
         const long long most = (long long)(kSmWarps / c.warps) * sms * (c.ctas > 1 ? 7 : 8) / 8, need = items * c.ctas;
@@ -664,13 +664,12 @@ void choose_clusters(Layout& r, long long items, int slots, int sms) {
         if (waves > 1 && (c.ctas > 1 || 2 * (need - (waves - 1) * most) < most)) continue;
         const int warps = c.warps * c.ctas;
         const long long rounds = waves * ((slots + warps - 1) / warps);
-        if (r.ctas && (rounds > best || (rounds == best && best > 1))) continue;
+        if (best && (rounds > best || (rounds == best && best > 1))) continue;
         best = rounds;
-        r.warps = c.warps;
-        r.ctas = c.ctas;
+        cta_warps = c.warps;
+        ctas = c.ctas;
     }
-    if (best > 1 && 2 * items * kClusters[0].warps * kClusters[0].ctas < (long long)kSmWarps * sms) r.ctas = 0;
-    if (r.ctas) r.grid = (int)(items * r.ctas);
+    return best == 1 || (best > 1 && 2 * items * kClusters[0].warps * kClusters[0].ctas >= (long long)kSmWarps * sms);
 }
 
 Layout layout(int N, int Hkv, int K) {
@@ -686,7 +685,12 @@ Layout layout(int N, int Hkv, int K) {
     const long long mn = r.V / r.ranges;                     // shortest range
     const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
     r.nslot = (int)(span < r.ranges ? span : r.ranges);
-    choose_clusters(r, (long long)N * Hkv, K + 1, sms);
+    int warps, ctas;
+    if (choose_clusters((long long)N * Hkv, K + 1, sms, warps, ctas)) {
+        r.warps = warps;
+        r.ctas = ctas;
+        r.grid = N * Hkv * ctas;
+    }
     return r;
 }
 
