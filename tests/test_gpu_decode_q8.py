@@ -143,8 +143,7 @@ def test_every_way_to_cut_the_work(Hq, Hkv, N, K):
 
 @pytest.mark.parametrize("N,Hq,Hkv,K", [(3, 24, 8, 620), (1, 8, 8, 1900), (3, 16, 8, 300), (2, 2, 1, 700)])
 def test_few_items_with_many_slots(N, Hq, Hkv, K):
-    """Fewer than 28 items: the device's ranges, of ten warps an SM from 14,800 slots on and of four below.
-    The sequences share pages."""
+    """Fewer than 28 items: the device's ranges, up to 25 slots long. The sequences share pages."""
     x = _make([64 * 20] * N, Hq, Hkv, 0, seed=40)
     g = torch.Generator().manual_seed(41)
     P, blocks = x["k_cache"].shape[0], K + 40

@@ -74,13 +74,10 @@ constexpr int kList = 64;                           // two batches of a warp
 // warps an SM (their rings are its shared memory).
 constexpr int kSmWarps = 12;
 // Without clusters the slots of all items are one line, cut into a range for each
-// warp of the device. Ten warps an SM with one stage each hide the math better than
-// four with three, but cut the slots into more ranges, whose lengths differ by one.
-// Measured (32/8 heads, ten against four): 65,600 slots 171.7 / 178.9 us, 21,120
-// slots 66.3 / 68.5, 12,672 slots 44.3 / 45.1, 6,336 slots 31.3 / 27.9. Ten from ten
-// slots a range on.
-constexpr int kManyWarps = 10, kFewWarps = 4;
-constexpr int kManySlots = 10;
+// warp of the device: a CTA of four warps with three stages each an SM. (Measured
+// against ten warps of one stage: 16,400 slots 51.9 / 55.1 us, 24,024 slots 71.3 / 71.5,
+// 77,400 slots 205 / 200.)
+constexpr int kRangeWarps = 4, kRangeStages = 3;
 
 // kWarps warps of a CTA, kDepth ring stages each, and their shared memory.
 template <int kWarps, int kDepth>
@@ -637,8 +634,7 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
 
 struct Layout {
     long long V;
-    int warps;                  // of a CTA
-    int ctas = 0;               // of a cluster; 0: ranges
+    int warps, ctas;            // of a cluster's CTA, of a cluster; ctas 0: ranges
     int grid, ranges, nslot;
 };
 constexpr struct {
@@ -678,19 +674,16 @@ Layout layout(int N, int Hkv, int K) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
     r.V = (long long)N * Hkv * (K + 1);
-    r.warps = r.V >= (long long)kManySlots * kManyWarps * sms ? kManyWarps : kFewWarps;
     r.grid = (int)(r.V < sms ? r.V : sms);
-    const long long most = (long long)sms * r.warps;
+    const long long most = (long long)sms * kRangeWarps;
     r.ranges = (int)(r.V < most ? r.V : most);
     const long long mn = r.V / r.ranges;                     // shortest range
     const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
     r.nslot = (int)(span < r.ranges ? span : r.ranges);
-    int warps, ctas;
-    if (choose_clusters((long long)N * Hkv, K + 1, sms, warps, ctas)) {
-        r.warps = warps;
-        r.ctas = ctas;
-        r.grid = N * Hkv * ctas;
-    }
+    if (choose_clusters((long long)N * Hkv, K + 1, sms, r.warps, r.ctas))
+        r.grid = N * Hkv * r.ctas;
+    else
+        r.ctas = 0;
     return r;
 }
 
@@ -762,12 +755,16 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
         if (e == cudaSuccess) count_launches(1);
         return e;
     }
-    e = lay.warps == kManyWarps ? launch<kManyWarps, 1>(lay, map, p, st) : launch<kFewWarps, 3>(lay, map, p, st);
+    e = launch<kRangeWarps, kRangeStages>(lay, map, p, st);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    e = launch_dependent(lay.nslot > 8 ? decode_q8_combine_kernel<4> : decode_q8_combine_kernel<1>, dim3((unsigned)(a.N * a.Hq)),
-                         lay.nslot > 8 ? 4 * kD : kD, 0, st, part_o, part_ml, lay.nslot, a.Hq, a.Hkv, p.G, a.K, lay.V,
-                         lay.ranges, (__nv_bfloat16*)a.o, a.lse);
+    // (501 partials of a row: 13.5 us with eight groups, 14.8 with four; 34 partials: 12.0, 11.5)
+    const int groups = lay.nslot > 128 ? 8 : lay.nslot > 8 ? 4 : 1;
+    const auto combine = groups == 8   ? decode_q8_combine_kernel<8>
+                         : groups == 4 ? decode_q8_combine_kernel<4>
+                                       : decode_q8_combine_kernel<1>;
+    e = launch_dependent(combine, dim3((unsigned)(a.N * a.Hq)), groups * kD, 0, st, part_o, part_ml, lay.nslot, a.Hq, a.Hkv, p.G,
+                         a.K, lay.V, lay.ranges, (__nv_bfloat16*)a.o, a.lse);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
