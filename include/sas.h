@@ -353,7 +353,8 @@ sas_status sas_decode_paged_noalloc(const void *q, const void *k_cache, const vo
                                     void *stream);
 
 /* Bytes of device workspace sas_decode_paged_q8 needs (0 on a bad argument; 256 where it
- * keeps nothing there). */
+ * keeps nothing there, as with most batches). Fewer sequences may need more than many:
+ * a workspace for several sizes has the largest of their sizes. */
 size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
 
 /*

@@ -341,6 +341,7 @@ def decode_paged(q, k_cache, v_cache, page_table, kv_len, idx, cnt, log_gate, sm
 
 
 def decode_q8_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, K: int) -> int:
+    """Workspace of decode_paged_q8 for exactly these sizes (fewer sequences may need more than many)."""
     return int(lib().sas_decode_q8_workspace_size(N, Hq, Hkv, D, K))
 
 
