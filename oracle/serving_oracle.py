@@ -132,14 +132,14 @@ def decode_q8(q, k_codes, v_codes, k_scale, v_scale, page_table, kv_len, idx, cn
                 o[n, hq] = p @ (vscale[:, None] * vcode)
                 lse[n, hq] = m + math.log(z)
                 # logits: D + 8 roundings of the dot product's terms, and eight of the
-                # sum's size (scales, gate, log2 of the value scale, maximum, exp2)
+                # sum's size (scale, gate, maximum, exp2)
                 dx = (D + 8) * u * sm_scale * kscale * (np.abs(kcode) @ np.abs(q[n, hq])) + \
-                    8 * u * (np.abs(x) + np.abs(np.log(vscale)) + np.abs(m) + 1)
+                    8 * u * (np.abs(x) + np.abs(m) + 1)
                 # probabilities: exp of such a logit; the sum and the value product add n + 8
                 # roundings; fp16 weights are 2^-11 off, or 2^-25 of the largest below 2^-14
                 rel = dx + dx.max() + (len(x) + 8) * u
-                top = (e * vscale).max()
-                w_err = p * vscale * (rel + 2.0 ** -11) + 2.0 ** -25 * top / z
-                o_tol[n, hq] = w_err @ np.abs(vcode) + 2.0 ** -8 * np.abs(o[n, hq])
+                w_err = p * vscale * (rel + 2.0 ** -11) + 2.0 ** -25 * vscale / z
+                # the blocks' products are added in units of 2^21, where fp32 ends at 2^-149
+                o_tol[n, hq] = w_err @ np.abs(vcode) + 2.0 ** -8 * np.abs(o[n, hq]) + len(blocks) * 2.0 ** -126
                 lse_tol[n, hq] = dx.max() + (len(x) + 8) * u + 8 * u * abs(lse[n, hq])
     return o, lse, o_tol * 1.01, lse_tol * 1.01

@@ -4,9 +4,11 @@
 // head): key = ks kc, value = vs vc. With gate g of a kept block (0 for the
 // current one) and x = sm_scale ks (q . kc) + g,
 //   o = sum_j e^(x_j - m) vs_j vc_j / sum_j e^(x_j - m),  lse = m + log(sum_j e^(x_j - m)).
-// The value scale goes into the exponent: with y = x log2(e) + log2(vs) and m the
-// running maximum of y, w = 2^(y - m) <= 1 is the weight of the code itself, so
-// that the value codes need no multiplication, and the softmax sum takes w / vs.
+// With y = x log2(e) and m the running maximum of y, w = 2^(y - m) <= 1. A block's
+// product of weights and value codes has accumulators of its own, which times vs
+// are added to those of the range: neither the weights nor the sum depend on the
+// scales, however far apart they lie. (Sums of codes times 2^128, the largest that
+// vs and 16-bit values allow, stay in range for 2^20 tokens: they are kept times 2^-21.)
 // Codes are exact in fp16, the queries are scaled by a power of two (their
 // largest element to 2^13 .. 2^14, what falls out of fp16 below is under 2^-30 of
 // it), the weights are rounded to fp16 (2^-11 relative); logits, sums and
@@ -64,10 +66,11 @@ struct Block {              // a resolved block of a warp's stream
     int tokens;             // rows to copy; 0: nothing to read
     int item;
     int nvalid;             // rows to attend: tokens, or 0 when the gate is closed or a scale out of range
-    float bias;             // gate + log2(vs), log2 units
-    float ks, inv_vs;
+    float bias;             // gate, log2 units
+    float ks, vs;           // vs times kUnit
     int pad;
 };
+constexpr float kUnit = 1.f / (1 << 21);            // of the accumulators
 constexpr int kList = 64;                           // two batches of a warp
 
 // A cluster of kCtas CTAs of kWarps warps with one stage each has one item: twelve
@@ -106,7 +109,7 @@ struct Params {
     long long V;            // n_items * (K + 1) block slots
     int ranges;
     int nslot;              // partial slots per query head
-    float* part_o;          // [N * Hq, nslot, D]
+    float* part_o;          // [N * Hq, nslot, D], times kUnit
     float* part_ml;         // [N * Hq, nslot, 2]
     __nv_bfloat16* o;       // [N, Hq, D]; lse [N, Hq] or null (clusters; else the combine writes them)
     float* lse;
@@ -228,10 +231,10 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
 __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b) {
     const bool ok = scale_ok(r.ks) && scale_ok(r.vs);
     if (!ok) flag_status(p.status, kStatusBadData);
-    b.bias = r.gate * kLog2e + log2f(r.vs);
+    b.bias = r.gate * kLog2e;
     b.nvalid = ok && b.bias != -INFINITY ? r.tokens : 0;     // behind a closed gate a NaN must not reach the sums
     b.ks = r.ks;
-    b.inv_vs = 1.f / r.vs;
+    b.vs = r.vs * kUnit;
 }
 
 // kCluster = 0: the ranges of the whole device, whose partials go to the workspace.
@@ -282,7 +285,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint32_t lofs = sw128_offset((lane & 7) + (lane & 8), lane >> 4);
     const uint32_t ring_s = smem_u32(ring) + lofs;
     uint32_t qb[8][2];          // Q^T as B fragments: 8 k-steps x (dims 4tig, +1 / +2, +3 of the step) of head grp
-    float o[8][4];              // O^T: tile mt, dims 16mt + 2grp (+1 in [2], [3]) x heads 2tig, 2tig + 1
+    float o[8][4];              // O^T times kUnit: tile mt, dims 16mt + 2grp (+1 in [2], [3]) x heads 2tig, 2tig + 1
     float m[2], l[2];           // heads 2tig, 2tig + 1: max of y; this lane's part of the sum
     float qm[2];                // sm_scale log2(e) over the query scale of those heads
 
@@ -483,7 +486,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 pb[mt][1] = transpose8x8(pack_f16x2(s[mt][2], s[mt][3]));
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], sc[e], ls[e] * b.inv_vs);
+            for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], sc[e], ls[e]);
             if (__any_sync(0xffffffffu, sc[0] != 1.f || sc[1] != 1.f)) {     // a maximum grew
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt)
@@ -491,18 +494,27 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     for (int e = 0; e < 4; ++e) o[mt][e] *= sc[e & 1];
             }
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
+            for (int mt = 0; mt < 8; mt += 2) {
+                float pv[2][4];         // O^T of this block, in codes
 #pragma unroll
-                for (int mt = 0; mt < 8; mt += 2) {
+                for (int e = 0; e < 4; ++e) pv[0][e] = pv[1][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
                     uint32_t r[4], a0, a1, a2, a3;
                     ldsm_x4_t((vt ^ (mt << 4)) + kk * 2048, r);
                     codes_f16(__byte_perm(r[0], 0u, 0x3120), a0, a1);
                     codes_f16(__byte_perm(r[1], 0u, 0x3120), a2, a3);
-                    mma16816(o[mt], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
+                    mma16816(pv[0], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
                     codes_f16(__byte_perm(r[2], 0u, 0x3120), a0, a1);
                     codes_f16(__byte_perm(r[3], 0u, 0x3120), a2, a3);
-                    mma16816(o[mt + 1], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
+                    mma16816(pv[1], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[mt][e] = fmaf(pv[0][e], b.vs, o[mt][e]);
+                    o[mt + 1][e] = fmaf(pv[1][e], b.vs, o[mt + 1][e]);
+                }
+            }
         }
         fence_proxy_async_smem();     // this stage's reads and zeroes before its next copy
         __syncwarp();
@@ -553,8 +565,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
             const bool none = M == -INFINITY;
             const long long row = (long long)n * p.Hq + h * p.G + g;
+            const float inv = (1.f / kUnit) / L;
             *reinterpret_cast<__nv_bfloat162*>(p.o + row * kD + d) =
-                none ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.x / L, acc.y / L);
+                none ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
             if (p.lse != nullptr && d == 0) p.lse[row] = none ? M : (M + log2f(L)) * kLn2;
         }
         cluster_sync<kCluster>();   // nobody leaves while its partials are read
@@ -628,7 +641,7 @@ decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restri
         }
     }
     const bool none = M == -INFINITY;
-    o[row * kD + d] = __float2bfloat16_rn(none ? 0.f : acc / L);
+    o[row * kD + d] = __float2bfloat16_rn(none ? 0.f : acc * ((1.f / kUnit) / L));
     if (lse != nullptr && d == 0) lse[row] = none ? M : (M + log2f(L)) * kLn2;
 }
 
