@@ -136,10 +136,14 @@ def decode_q8(q, k_codes, v_codes, k_scale, v_scale, page_table, kv_len, idx, cn
                 dx = (D + 8) * u * sm_scale * kscale * (np.abs(kcode) @ np.abs(q[n, hq])) + \
                     8 * u * (np.abs(x) + np.abs(m) + 1)
                 # probabilities: exp of such a logit; the sum and the value product add n + 8
-                # roundings; fp16 weights are 2^-11 off, or 2^-25 of the largest below 2^-14
-                rel = dx + dx.max() + (len(x) + 8) * u
-                w_err = p * vscale * (rel + 2.0 ** -11) + 2.0 ** -25 * vscale / z
-                # the blocks' products are added in units of 2^21, where fp32 ends at 2^-149
+                # roundings; fp16 weights, the largest of which is 2^15, are 2^-11 off, or 2^-25
+                # in the subnormal range (2^-40 of the largest; 2^-39 where 15 itself is rounded)
+                # the blocks' products are added times 2^-36: scales below 2^-90 are
+                # subnormal then, half a step of 2^-149 off; so are the smallest sums
+                rel = dx + dx.max() + (len(x) + 8) * u + np.where(vscale < 2.0 ** -90, 2.0 ** -150 / (vscale * 2.0 ** -36), 0)
+                w_err = p * vscale * (rel + 2.0 ** -11) + 2.0 ** -39 * vscale / z
                 o_tol[n, hq] = w_err @ np.abs(vcode) + 2.0 ** -8 * np.abs(o[n, hq]) + len(blocks) * 2.0 ** -126
-                lse_tol[n, hq] = dx.max() + (len(x) + 8) * u + 8 * u * abs(lse[n, hq])
+                # the sum is of weights up to 2^15: exponents of that size (half a step, 8 u, times
+                # ln 2) and a logarithm of up to 31 (a step of it, 32 u, times ln 2)
+                lse_tol[n, hq] = dx.max() + (len(x) + 8) * u + 8 * u * abs(lse[n, hq]) + 28 * u
     return o, lse, o_tol * 1.01, lse_tol * 1.01

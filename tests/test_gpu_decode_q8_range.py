@@ -93,3 +93,13 @@ def test_a_page_with_one_channel_far_out():
     x["v_scale"][:] = 2.0 ** -8
     x["v_scale"][0] = 2.0 ** 6
     _check(_run(x), _ref(x))
+
+
+def test_small_weights_beside_one_large():
+    """12,800 tokens of weights e^-18 and below behind a block whose values are zero: o is theirs alone."""
+    x = shared(64, 8, 8, 200, 230, seed=80)
+    x["page_table"][:, 1:] = x["page_table"][:, 1:].clamp(min=1)
+    x["page_table"][:, 0] = x["page_table"][:, -1] = 0          # the first kept and the current block
+    x["v_cache"].view(torch.uint8)[0] = 0
+    x["log_gate"][:, :, 0], x["log_gate"][:, :, 1:] = 0.0, -18.0
+    _check(_run(x), _ref(x))

@@ -4,11 +4,13 @@
 // head): key = ks kc, value = vs vc. With gate g of a kept block (0 for the
 // current one) and x = sm_scale ks (q . kc) + g,
 //   o = sum_j e^(x_j - m) vs_j vc_j / sum_j e^(x_j - m),  lse = m + log(sum_j e^(x_j - m)).
-// With y = x log2(e) and m the running maximum of y, w = 2^(y - m) <= 1. A block's
-// product of weights and value codes has accumulators of its own, which times vs
-// are added to those of the range: neither the weights nor the sum depend on the
-// scales, however far apart they lie. (Sums of codes times 2^128, the largest that
-// vs and 16-bit values allow, stay in range for 2^20 tokens: they are kept times 2^-21.)
+// With y = x log2(e) and m the running maximum of y, w = 2^(y - m + 15): the largest
+// weight is 2^15, near the top of fp16, so that weights keep all 11 bits down to
+// 2^-29 of it, and some down to 2^-39. A block's product of weights and value codes
+// has accumulators of its own, which times vs are added to those of the range:
+// neither the weights nor the sum depend on the scales, however far apart they lie.
+// (Sums of codes times 2^128, the largest that vs and 16-bit values allow, stay in
+// range for 2^20 tokens: they are kept times 2^-36.)
 // Codes are exact in fp16, the queries are scaled by a power of two (their
 // largest element to 2^13 .. 2^14, what falls out of fp16 below is under 2^-30 of
 // it), the weights are rounded to fp16 (2^-11 relative); logits, sums and
@@ -70,7 +72,12 @@ struct Block {              // a resolved block of a warp's stream
     float ks, vs;           // vs times kUnit
     int pad;
 };
-constexpr float kUnit = 1.f / (1 << 21);            // of the accumulators
+constexpr float kUnit = 1.f / (1LL << 36);          // of the accumulators
+
+// What a weight's exponent is taken against, with m the largest of the exponents: 15 below m.
+// (Beyond 2^24 that difference would be rounded by more than fp16 has room for. Exponents
+// are whole numbers there, and the weights stay at 1 or below.)
+__device__ __forceinline__ float weight_ref(float m) { return fabsf(m) < 16777216.f ? m - 15.f : m; }
 constexpr int kList = 64;                           // two batches of a warp
 
 // A cluster of kCtas CTAs of kWarps warps with one stage each has one item: twelve
@@ -88,7 +95,7 @@ struct Shape {
     static constexpr uint32_t kOffList = kWarps * kDepth * kStageBytes;
     static constexpr uint32_t kOffBar = kOffList + kWarps * kList * sizeof(Block);
     static constexpr uint32_t kOffAbort = kOffBar + kWarps * kDepth * 8;
-    static constexpr uint32_t kOffMl = (kOffAbort + kWarps * 4 + 7) / 8 * 8;     // a warp's max and sum for each head
+    static constexpr uint32_t kOffMl = (kOffAbort + kWarps * 4 + 7) / 8 * 8;     // a warp's weight_ref and sum for each head
     static constexpr uint32_t kSmem = kOffMl + kWarps * 8 * sizeof(float2) + 1024;       // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -286,7 +293,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint32_t ring_s = smem_u32(ring) + lofs;
     uint32_t qb[8][2];          // Q^T as B fragments: 8 k-steps x (dims 4tig, +1 / +2, +3 of the step) of head grp
     float o[8][4];              // O^T times kUnit: tile mt, dims 16mt + 2grp (+1 in [2], [3]) x heads 2tig, 2tig + 1
-    float m[2], l[2];           // heads 2tig, 2tig + 1: max of y; this lane's part of the sum
+    float m[2], mr[2], l[2];    // heads 2tig, 2tig + 1: max of y and its weight_ref; this lane's part of the sum
     float qm[2];                // sm_scale log2(e) over the query scale of those heads
 
     auto start = [&](int item) {
@@ -319,7 +326,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         qm[1] = __shfl_sync(0xffffffffu, qi, 8 * tig + 4);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
+        m[0] = m[1] = mr[0] = mr[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     };
     // row of the item's first query head, at this range's partial slot
@@ -334,16 +341,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             ml[1] = 0.f;
         }
     };
-    // row g's partial: its max and sum to ml + g * stride, its accumulators to o_out + g * stride * D
+    // row g's partial: weight_ref and sum to ml + g * stride, its accumulators to o_out + g * stride * D
     auto write_to = [&](float2* ml, float* o_out, int stride) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
-            if (l[e] != l[e]) m[e] = fmaxf(m[e], -1e30f);     // only NaN logits: the row is not an empty one
+            if (l[e] != l[e]) mr[e] = fmaxf(mr[e], -1e30f);   // only NaN logits: the row is not an empty one
             const int g = 2 * tig + e;
             if (g >= p.G) continue;
-            if (grp == 0) ml[(long long)g * stride] = make_float2(m[e], l[e]);
+            if (grp == 0) ml[(long long)g * stride] = make_float2(mr[e], l[e]);
             float* dst = o_out + (long long)g * stride * kD + 2 * grp;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) *reinterpret_cast<float2*>(dst + 16 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
@@ -469,10 +476,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], x));
-                const float mn = fmaxf(m[e], bm[e]);
-                mu[e] = mn == -INFINITY ? 0.f : mn;              // a block of closed gates: 2^(-inf - 0) = 0
-                sc[e] = fast_exp2(m[e] - mu[e]);
-                m[e] = mn;
+                m[e] = fmaxf(m[e], bm[e]);
+                const float ref = weight_ref(m[e]);
+                mu[e] = ref == -INFINITY ? 0.f : ref;            // no finite logit yet: 2^(-inf - 0) = 0
+                sc[e] = fast_exp2(mr[e] - mu[e]);
+                mr[e] = ref;
             }
             uint32_t pb[4][2];          // P^T as B fragments
 #pragma unroll
