@@ -371,8 +371,8 @@ size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
  * log_gate   -inf (or the lowest fp32 value) leaves its block out, whatever its page
  *            holds. A block that idx names twice is attended twice.
  * Other arguments as in sas_decode_paged. Logits, softmax sums and accumulators are
- * fp32; in front of the value product probabilities are rounded to fp16's 11 bits (down
- * to 2^-29 of the row's largest; fewer down to 2^-39, below they count in lse alone).
+ * fp32; in front of the value product probabilities are rounded to 21 bits or more (those
+ * under 2^-29 of the row's largest to fewer, under 2^-39 they count in lse alone).
  * A sequence without a readable block gets o 0 and lse -inf.
  * workspace  device, ws_bytes >= sas_decode_q8_workspace_size(...), 256-byte
  *            aligned; contents on entry do not matter.

@@ -136,12 +136,13 @@ def decode_q8(q, k_codes, v_codes, k_scale, v_scale, page_table, kv_len, idx, cn
                 dx = (D + 8) * u * sm_scale * kscale * (np.abs(kcode) @ np.abs(q[n, hq])) + \
                     8 * u * (np.abs(x) + np.abs(m) + 1)
                 # probabilities: exp of such a logit; the sum and the value product add n + 8
-                # roundings; fp16 weights, the largest of which is 2^15, are 2^-11 off, or 2^-25
-                # in the subnormal range (2^-40 of the largest; 2^-39 where 15 itself is rounded)
+                # roundings; weights, the largest of which is 2^15, as two fp16 numbers are 2^-21
+                # off, or 2^-25 for each number in the subnormal range (2^-39 of the largest; 2^-38
+                # where 15 itself is rounded)
                 # the blocks' products are added times 2^-36: scales below 2^-90 are
                 # subnormal then, half a step of 2^-149 off; so are the smallest sums
                 rel = dx + dx.max() + (len(x) + 8) * u + np.where(vscale < 2.0 ** -90, 2.0 ** -150 / (vscale * 2.0 ** -36), 0)
-                w_err = p * vscale * (rel + 2.0 ** -11) + 2.0 ** -39 * vscale / z
+                w_err = p * vscale * (rel + 2.0 ** -21) + 2.0 ** -38 * vscale / z
                 o_tol[n, hq] = w_err @ np.abs(vcode) + 2.0 ** -8 * np.abs(o[n, hq]) + len(blocks) * 2.0 ** -126
                 # the sum is of weights up to 2^15: exponents of that size (half a step, 8 u, times
                 # ln 2) and a logarithm of up to 31 (a step of it, 32 u, times ln 2)

@@ -103,3 +103,14 @@ def test_small_weights_beside_one_large():
     x["v_cache"].view(torch.uint8)[0] = 0
     x["log_gate"][:, :, 0], x["log_gate"][:, :, 1:] = 0.0, -18.0
     _check(_run(x), _ref(x))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (3, 1), (10, 2), (8, 1)])
+def test_values_that_cancel(Hq, Hkv):
+    """Two tokens of nearly equal weights and opposite values: what the weights lose would show in o."""
+    x = _make([2] * 64, Hq, Hkv, 0, seed=90)
+    x["q"] = x["q"] * 0.005
+    raw = (x["v_cache"].view(torch.uint8) | 0x60) & 0x7e            # codes of 32 to 448
+    raw[:, :, 1] = raw[:, :, 0] | 0x80
+    x["v_cache"] = raw.view(x["v_cache"].dtype)
+    _check(_run(x), _ref(x))

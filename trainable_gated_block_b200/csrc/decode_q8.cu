@@ -5,7 +5,7 @@
 // current one) and x = sm_scale ks (q . kc) + g,
 //   o = sum_j e^(x_j - m) vs_j vc_j / sum_j e^(x_j - m),  lse = m + log(sum_j e^(x_j - m)).
 // With y = x log2(e) and m the running maximum of y, w = 2^(y - m + 15): the largest
-// weight is 2^15, near the top of fp16, so that weights keep all 11 bits down to
+// weight is 2^15, near the top of fp16, so that weights keep all bits down to
 // 2^-29 of it, and some down to 2^-39. A block's product of weights and value codes
 // has accumulators of its own, which times vs are added to those of the range:
 // neither the weights nor the sum depend on the scales, however far apart they lie.
@@ -13,8 +13,10 @@
 // range for 2^20 tokens: they are kept times 2^-36.)
 // Codes are exact in fp16, the queries are scaled by a power of two (their
 // largest element to 2^13 .. 2^14, what falls out of fp16 below is under 2^-30 of
-// it), the weights are rounded to fp16 (2^-11 relative); logits, sums and
-// accumulators are fp32.
+// it), a weight is the sum of two fp16 numbers (2^-21 relative: one alone, 2^-11 off,
+// let one output in 50 round to another bf16 number); logits, sums and accumulators
+// are fp32. The second numbers' product costs nothing where up to four heads share a
+// KV head, since they take the columns that these leave empty.
 //
 // HBM-bound design. Each (sequence, KV head) item has K + 1 slots: its kept blocks and
 // the current one. The warps of a cluster of one to eight CTAs cut an item's slots
@@ -45,6 +47,8 @@
 // variant with a producer warp, consumers that meet at each item's end and
 // one exp2f for each logit took 237 and 81.6 us: its math did not keep up.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "byte_map.h"
 #include "common.cuh"
@@ -189,6 +193,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The part of a weight that fp16's 11 bits hold.
+__device__ __forceinline__ float upper(float w) { return __uint_as_float(__float_as_uint(w) & 0xffffe000u); }
+
 // A block slot: whether it holds a kept or current block, that block's tile, and
 // its gate and scales as loaded (finish() comes after the tile's copy is under way).
 struct Slot {
@@ -287,6 +294,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     int cur_item = kCluster == 0 ? (int)(v / Kp1) : own_item;
 
     const int grp = lane >> 2, tig = lane & 3;     // mma fragment coordinates
+    const bool few_heads = p.G <= 4;               // columns 4..7 are the same heads as 0..3, for the weights' lower parts
     // ldmatrix: this lane's row within 16 keys; chunk c of that row is at lofs ^ (c << 4) (c even; the odd
     // chunk of the pair goes to the upper lanes)
     const uint32_t lofs = sw128_offset((lane & 7) + (lane & 8), lane >> 4);
@@ -298,8 +306,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
     auto start = [&](int item) {
         const int n = item / p.Hkv, h = item % p.Hkv;
-        const bool real = grp < p.G;
-        const uint2* qrow = reinterpret_cast<const uint2*>(p.q + ((long long)n * p.Hq + h * p.G + (real ? grp : 0)) * kD);
+        const int g = few_heads ? grp & 3 : grp;
+        const bool real = g < p.G;
+        const uint2* qrow = reinterpret_cast<const uint2*>(p.q + ((long long)n * p.Hq + h * p.G + (real ? g : 0)) * kD);
         uint2 qr[8];
         float top = 0.f;
 #pragma unroll
@@ -343,6 +352,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     };
     // row g's partial: weight_ref and sum to ml + g * stride, its accumulators to o_out + g * stride * D
     auto write_to = [&](float2* ml, float* o_out, int stride) {
+        if (few_heads) {
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][e] += __shfl_xor_sync(0xffffffffu, o[mt][e], 2);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -482,17 +497,13 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 sc[e] = fast_exp2(mr[e] - mu[e]);
                 mr[e] = ref;
             }
-            uint32_t pb[4][2];          // P^T as B fragments
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
+            for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[mt][e] = fast_exp2(s[mt][e] - mu[e & 1]);
                     ls[e & 1] += s[mt][e];
                 }
-                pb[mt][0] = transpose8x8(pack_f16x2(s[mt][0], s[mt][1]));
-                pb[mt][1] = transpose8x8(pack_f16x2(s[mt][2], s[mt][3]));
-            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) l[e] = fmaf(l[e], sc[e], ls[e]);
             if (__any_sync(0xffffffffu, sc[0] != 1.f || sc[1] != 1.f)) {     // a maximum grew
@@ -501,28 +512,52 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][e] *= sc[e & 1];
             }
+            // O^T of this block. P^T as B fragments: the weights' upper parts and what is left
+            // of them, in the columns of the heads and those behind or one after the other
+            auto product = [&](auto side_by_side) {
+                constexpr int kParts = decltype(side_by_side)::value ? 1 : 2;
+                uint32_t pb[kParts][4][2];
 #pragma unroll
-            for (int mt = 0; mt < 8; mt += 2) {
-                float pv[2][4];         // O^T of this block, in codes
+                for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pv[0][e] = pv[1][e] = 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        const float w0 = s[mt][2 * e], w1 = s[mt][2 * e + 1], u0 = upper(w0), u1 = upper(w1);
+                        if (kParts == 1) {
+                            pb[0][mt][e] = transpose8x8(tig < 2 ? pack_f16x2(u0, u1) : pack_f16x2(w0 - u0, w1 - u1));
+                        } else {
+                            pb[0][mt][e] = transpose8x8(pack_f16x2(u0, u1));
+                            pb[kParts - 1][mt][e] = transpose8x8(pack_f16x2(w0 - u0, w1 - u1));
+                        }
+                    }
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    uint32_t r[4], a0, a1, a2, a3;
-                    ldsm_x4_t((vt ^ (mt << 4)) + kk * 2048, r);
-                    codes_f16(__byte_perm(r[0], 0u, 0x3120), a0, a1);
-                    codes_f16(__byte_perm(r[1], 0u, 0x3120), a2, a3);
-                    mma16816(pv[0], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
-                    codes_f16(__byte_perm(r[2], 0u, 0x3120), a0, a1);
-                    codes_f16(__byte_perm(r[3], 0u, 0x3120), a2, a3);
-                    mma16816(pv[1], a0, a1, a2, a3, pb[kk][0], pb[kk][1]);
+                for (int mt = 0; mt < 8; mt += 2) {
+                    float pv[2][4];     // in codes
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pv[0][e] = pv[1][e] = 0.f;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        uint32_t r[4], a0, a1, a2, a3;
+                        ldsm_x4_t((vt ^ (mt << 4)) + kk * 2048, r);
+                        codes_f16(__byte_perm(r[0], 0u, 0x3120), a0, a1);
+                        codes_f16(__byte_perm(r[1], 0u, 0x3120), a2, a3);
+#pragma unroll
+                        for (int i = 0; i < kParts; ++i) mma16816(pv[0], a0, a1, a2, a3, pb[i][kk][0], pb[i][kk][1]);
+                        codes_f16(__byte_perm(r[2], 0u, 0x3120), a0, a1);
+                        codes_f16(__byte_perm(r[3], 0u, 0x3120), a2, a3);
+#pragma unroll
+                        for (int i = 0; i < kParts; ++i) mma16816(pv[1], a0, a1, a2, a3, pb[i][kk][0], pb[i][kk][1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[mt][e] = fmaf(pv[0][e], b.vs, o[mt][e]);
+                        o[mt + 1][e] = fmaf(pv[1][e], b.vs, o[mt + 1][e]);
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[mt][e] = fmaf(pv[0][e], b.vs, o[mt][e]);
-                    o[mt + 1][e] = fmaf(pv[1][e], b.vs, o[mt + 1][e]);
-                }
-            }
+            };
+            if (few_heads)
+                product(std::true_type());
+            else
+                product(std::false_type());
         }
         fence_proxy_async_smem();     // this stage's reads and zeroes before its next copy
         __syncwarp();
