@@ -368,8 +368,8 @@ size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
  *            and 2^120 for every page that is read; any other scale is flagged and
  *            its block skipped, like a bad page id.
  * kv_len     as in sas_decode_paged; 0 is a padding entry: o 0, lse -inf, not flagged.
- * log_gate   -inf (or the lowest fp32 value) leaves its block out, whatever its page
- *            holds. A block that idx names twice is attended twice.
+ * log_gate   -inf (or the lowest fp32 value) leaves its block out: its page id, scales
+ *            and page are not looked at. A block that idx names twice is attended twice.
  * Other arguments as in sas_decode_paged. Logits, softmax sums and accumulators are
  * fp32; in front of the value product probabilities are rounded to 21 bits or more (those
  * under 2^-29 of the row's largest to fewer, under 2^-39 they count in lse alone).

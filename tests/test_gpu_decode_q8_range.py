@@ -114,3 +114,27 @@ def test_values_that_cancel(Hq, Hkv):
     raw[:, :, 1] = raw[:, :, 0] | 0x80
     x["v_cache"] = raw.view(x["v_cache"].dtype)
     _check(_run(x), _ref(x))
+
+
+def test_a_closed_block_is_left_out_whatever_its_page_and_scales():
+    """Behind a gate of -inf or the lowest fp32 value, pages with scales without a value and page ids outside the
+    cache are neither read nor flagged."""
+    x = _make([64 * 6 + 10, 64 * 5 + 1, 64 * 4], 4, 2, 4, seed=95)
+    for n in range(3):
+        x["idx"][n, 1], x["cnt"][n, 1] = x["idx"][n, 0], x["cnt"][n, 0]
+    low = torch.finfo(torch.float32).min
+    x["log_gate"][0, :, 1], x["log_gate"][0, :, 2], x["log_gate"][1, :, 0] = -math.inf, low, low
+    x["log_gate"][2, :, :3] = -math.inf
+    want = _run(x)
+    _check(want, _ref(dict(x, log_gate=torch.where(x["log_gate"] == low, -math.inf, x["log_gate"]))))
+    closed = [(0, 1), (0, 2), (1, 0), (2, 0), (2, 1), (2, 2)]
+    bad = [0.0, float("nan"), math.inf, -1.0, None, None]
+    for (n, i), b in zip(closed, bad):
+        block = int(x["idx"][n, 0, i])
+        page = int(x["page_table"][n, block])
+        if b is None:
+            x["page_table"][n, block] = -5 if i == 1 else x["k_cache"].shape[0]
+        else:
+            x["k_scale"][page], x["v_scale"][page] = b, b
+    got = _run(x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -71,7 +71,7 @@ struct Block {              // a resolved block of a warp's stream
     int row0;               // first cache row of its tile
     int tokens;             // rows to copy; 0: nothing to read
     int item;
-    int nvalid;             // rows to attend: tokens, or 0 when the gate is closed or a scale out of range
+    int nvalid;             // rows to attend: tokens, or 0 when a scale is out of range
     float bias;             // gate, log2 units
     float ks, vs;           // vs times kUnit
     int pad;
@@ -197,7 +197,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float upper(float w) { return __uint_as_float(__float_as_uint(w) & 0xffffe000u); }
 
 // A block slot: whether it holds a kept or current block, that block's tile, and
-// its gate and scales as loaded (finish() comes after the tile's copy is under way).
+// its gate (in log2 units) and scales (finish() comes after the tile's copy is under way).
 struct Slot {
     bool use;
     int row0, tokens, item;
@@ -226,9 +226,11 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
     const int n_sel = max(0, min(cnt, min(p.K, c)));
     if (n_sel != cnt) flag_status(p.status, kStatusBadData);
     if (t > n_sel) return r;
-    r.use = true;
     const bool cur = t == n_sel;
     if (cur) j = c;
+    r.gate = cur ? 0.f : gate * kLog2e;
+    if (r.gate == -INFINITY && j >= 0 && j < c) return r;        // a closed gate: nothing of the block is looked at
+    r.use = true;
     int page = -1;
     if (j >= 0 && j < c + cur) page = __ldg(p.page_table + (long long)n * p.max_pages + j);   // j <= c < max_pages
     if (page < 0 || page >= p.num_pages) {
@@ -237,7 +239,6 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
     }
     r.row0 = (page * p.Hkv + h) * kBlock;                        // < 2^31 (checked on the host)
     r.tokens = cur ? L - c * kBlock : kBlock;
-    r.gate = cur ? 0.f : gate;
     r.ks = __ldg(p.k_scale + (long long)page * p.Hkv + h);
     r.vs = __ldg(p.v_scale + (long long)page * p.Hkv + h);
     return r;
@@ -245,8 +246,8 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
 __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b) {
     const bool ok = scale_ok(r.ks) && scale_ok(r.vs);
     if (!ok) flag_status(p.status, kStatusBadData);
-    b.bias = r.gate * kLog2e;
-    b.nvalid = ok && b.bias != -INFINITY ? r.tokens : 0;     // behind a closed gate a NaN must not reach the sums
+    b.bias = r.gate;
+    b.nvalid = ok ? r.tokens : 0;
     b.ks = r.ks;
     b.vs = r.vs * kUnit;
 }
