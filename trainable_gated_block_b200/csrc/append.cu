@@ -47,8 +47,8 @@ using bf16 = __nv_bfloat16;
 
 __device__ __forceinline__ SeqNew load_seq(const AppendArgs& a, int n) {
     const bool cu = a.cu_new != nullptr;
-    return seq_new(cu, cu ? __ldg(a.cu_new + n) : 0, cu ? __ldg(a.cu_new + n + 1) : 0, n, a.T, a.max_new,
-                   __ldg(a.kv_len + n), a.max_pages, a.max_pos);
+    return seq_new(cu, cu ? a.cu_new[n] : 0, cu ? a.cu_new[n + 1] : 0, n, a.T, a.max_new,
+                   a.kv_len[n], a.max_pages, a.max_pos);
 }
 
 // Sequence that owns token row t, or -1.
@@ -57,9 +57,9 @@ __device__ __forceinline__ int seq_of_row(const AppendArgs& a, long long t) {
     int lo = 0, hi = a.N;                        // the last n with cu[n] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu_new + mid) <= t) lo = mid; else hi = mid;
+        if (a.cu_new[mid] <= t) lo = mid; else hi = mid;
     }
-    return __ldg(a.cu_new + lo) <= t && t < __ldg(a.cu_new + lo + 1) ? lo : -1;
+    return a.cu_new[lo] <= t && t < a.cu_new[lo + 1] ? lo : -1;
 }
 
 // Position of token row t: -1 for a padding entry, whose rows are zero; -2 for rows
@@ -288,7 +288,7 @@ __device__ __forceinline__ void token_kv(const AppendArgs& a, uint32_t u) {
         return;
     }
     const PageTile t = page_tile(s, 0);             // the one new row is t.lo
-    const int page = __ldg(a.page_table + (long long)n * a.max_pages + t.block);   // block < max_pages by kv_len's check
+    const int page = a.page_table[(long long)n * a.max_pages + t.block];   // block < max_pages by kv_len's check
     const bf16* src = (is_v ? static_cast<const bf16*>(a.v) + t.row * a.ld_v : static_cast<const bf16*>(a.k) + t.row * a.ld_k) +
                       h * D + 8 * l;
     const uint4 lo[1] = {ld_stream(src)}, hi[1] = {ld_stream(src + D / 2)};
@@ -365,8 +365,8 @@ struct SeqAt {
         count = s.count;
         first = s.first;
         bad = s.bad;
-        tile0 = seq_tile_base(__ldg(a.cu_new + at), at);
-        tile1 = seq_tile_base(__ldg(a.cu_new + at + 1), at + 1);
+        tile0 = seq_tile_base(a.cu_new[at], at);
+        tile1 = seq_tile_base(a.cu_new[at + 1], at + 1);
     }
     __device__ __forceinline__ bool holds(int t) const { return n >= 0 && !bad && t >= row0 && t - row0 < count; }
     // Goes to the sequence of token row t; false for a row of none, or of one that is skipped.
@@ -388,7 +388,7 @@ struct SeqAt {
             int lo = 0, hi = a.N;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (seq_tile_base(__ldg(a.cu_new + mid), mid) <= v) lo = mid; else hi = mid;
+                if (seq_tile_base(a.cu_new[mid], mid) <= v) lo = mid; else hi = mid;
             }
             load(a, lo);
         }
@@ -396,7 +396,7 @@ struct SeqAt {
         return page_tile(SeqNew{row0, first, count, false}, (int)(v - tile0));
     }
     __device__ __forceinline__ int page(const AppendArgs& a, int block) const {     // block < max_pages by kv_len's check
-        return __ldg(a.page_table + (long long)n * a.max_pages + block);
+        return a.page_table[(long long)n * a.max_pages + block];
     }
 };
 // Flags every sequence that breaks the call's terms, also those that no token row
@@ -404,7 +404,7 @@ struct SeqAt {
 __device__ __forceinline__ void flag_sequences(const AppendArgs& a) {
     if (blockIdx.x != 0) return;
     for (int n = threadIdx.x; n < a.N; n += blockDim.x)
-        if (load_seq(a, n).bad || __ldg(a.cu_new + n + 1) < __ldg(a.cu_new + n)) flag_status(a.status, kStatusBadData);
+        if (load_seq(a, n).bad || a.cu_new[n + 1] < a.cu_new[n]) flag_status(a.status, kStatusBadData);
 }
 
 enum UnitKind { kNone, kQ, kK, kV };

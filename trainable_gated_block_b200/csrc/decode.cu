@@ -415,10 +415,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 }
 
 __global__ void __launch_bounds__(kD)
-decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int nslot, int Hq, int Hkv,
-                      int G, int K, long long V, int grid, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+decode_combine_kernel(const float* part_o, const float* part_ml, int nslot, int Hq, int Hkv, int G, int K, long long V,
+                      int grid, __nv_bfloat16* o, float* lse) {
     // launched as a programmatic dependent of decode_kernel: its blocks may be
-    // resident before the decode grid ends; wait for that grid's writes here
+    // resident before the decode grid ends; wait for that grid's writes here (which
+    // may not be read by the read-only path: dependent.cuh)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long row = blockIdx.x;          // n * Hq + hq
     const int d = threadIdx.x;

@@ -214,10 +214,10 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
     r.item = (int)(v / Kp1);
     const int n = r.item / p.Hkv, h = r.item % p.Hkv;
     // independent loads first: an entry that turns out not to be one is not used
-    const int L = __ldg(p.kv_len + n), cnt = __ldg(p.cnt + r.item);
+    const int L = p.kv_len[n], cnt = p.cnt[r.item];
     const long long srow = (long long)r.item * p.K + t;
-    int j = t < p.K ? __ldg(p.idx + srow) : -1;
-    const float gate = t < p.K ? __ldg(p.log_gate + srow) : 0.f;
+    int j = t < p.K ? p.idx[srow] : -1;
+    const float gate = t < p.K ? p.log_gate[srow] : 0.f;
     if (L < 1 || L > (long long)p.max_pages * kBlock) {
         if (L != 0) flag_status(p.status, kStatusBadData);       // 0: a padding entry
         return r;
@@ -232,15 +232,15 @@ __device__ __forceinline__ Slot resolve(const Params& p, long long v) {
     if (r.gate == -INFINITY && j >= 0 && j < c) return r;        // a closed gate: nothing of the block is looked at
     r.use = true;
     int page = -1;
-    if (j >= 0 && j < c + cur) page = __ldg(p.page_table + (long long)n * p.max_pages + j);   // j <= c < max_pages
+    if (j >= 0 && j < c + cur) page = p.page_table[(long long)n * p.max_pages + j];   // j <= c < max_pages
     if (page < 0 || page >= p.num_pages) {
         flag_status(p.status, kStatusBadData);
         return r;
     }
     r.row0 = (page * p.Hkv + h) * kBlock;                        // < 2^31 (checked on the host)
     r.tokens = cur ? L - c * kBlock : kBlock;
-    r.ks = __ldg(p.k_scale + (long long)page * p.Hkv + h);
-    r.vs = __ldg(p.v_scale + (long long)page * p.Hkv + h);
+    r.ks = p.k_scale[(long long)page * p.Hkv + h];
+    r.vs = p.v_scale[(long long)page * p.Hkv + h];
     return r;
 }
 __device__ __forceinline__ void finish(const Params& p, const Slot& r, Block& b) {
@@ -313,7 +313,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         uint2 qr[8];
         float top = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) qr[kk] = real ? __ldg(qrow + 4 * kk + tig) : make_uint2(0u, 0u);
+        for (int kk = 0; kk < 8; ++kk) qr[kk] = real ? qrow[4 * kk + tig] : make_uint2(0u, 0u);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
             const float2 a = bf16x2_to_f32(qr[kk].x), b = bf16x2_to_f32(qr[kk].y);
@@ -625,8 +625,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 // gets 0 and an lse of -inf.
 template <int kGroups>
 __global__ void __launch_bounds__(kD* kGroups)
-decode_q8_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int nslot, int Hq, int Hkv,
-                         int G, int K, long long V, int ranges, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+decode_q8_combine_kernel(const float* part_o, const float* part_ml, int nslot, int Hq, int Hkv,
+                         int G, int K, long long V, int ranges, __nv_bfloat16* o, float* lse) {
     __shared__ float acc_s[kGroups][kD];
     __shared__ float2 ml_s[kGroups];
     after_previous();

@@ -2,7 +2,11 @@
 // in front of it in the stream (programmatic dependent launch). Every kernel
 // launched this way calls after_previous() before it touches memory, which
 // waits until that kernel has finished and its writes are visible: only the
-// placement of the CTAs comes early. In a stream of calls this saves one to two
+// placement of the CTAs comes early. It reads global memory by ordinary loads, which
+// that wait orders: not by the read-only path (__ldg, ld.global.nc, or const
+// __restrict__ parameters, which the compiler reads so), which is for memory that
+// nobody writes while the kernel runs, and the kernel in front may write what this one
+// reads when it has been placed already. In a stream of calls this saves one to two
 // microseconds a kernel (a ragged append 20.5 -> 18.5 us). Early CTAs go
 // where the kernel in front leaves room first: a persistent grid of several CTAs an
 // SM needs shared memory that lets no more of them onto an SM (norm + rotation of 8k

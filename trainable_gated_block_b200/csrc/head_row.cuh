@@ -68,9 +68,10 @@ template <> struct Raw8<float> {
 };
 
 // Inputs are read once: they bypass L1, which the rotation table's rows are to stay in.
+// (Not by the read-only path, as all loads of these kernels: dependent.cuh.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 w;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                  : "l"(p));
     return w;
@@ -138,7 +139,7 @@ __device__ __forceinline__ Angles load_angles(const float* table, int pos, int l
     // in 16-byte pieces: the second four dimensions of the lane's eight follow the first, or lie D / 4 further
     constexpr int kSecond = sizeof(T) == 2 ? 1 : D / 16;
     const ulonglong2* row = reinterpret_cast<const ulonglong2*>(table + (long long)pos * D + Raw8<T>::kStep * l);
-    const ulonglong2 c0 = __ldg(row), c1 = __ldg(row + kSecond), s0 = __ldg(row + D / 8), s1 = __ldg(row + D / 8 + kSecond);
+    const ulonglong2 c0 = row[0], c1 = row[kSecond], s0 = row[D / 8], s1 = row[D / 8 + kSecond];
     Angles g;
     g.c.v[0] = c0.x, g.c.v[1] = c0.y, g.c.v[2] = c1.x, g.c.v[3] = c1.y;
     g.s.v[0] = s0.x, g.s.v[1] = s0.y, g.s.v[2] = s1.x, g.s.v[3] = s1.y;
@@ -159,8 +160,8 @@ __device__ __forceinline__ Row load_weight(const T* w, int l) {
 #pragma unroll
     for (int i = 0; i < Raw8<T>::kPieces; ++i) {
         const T* at = w + i * (D / 4) + Raw8<T>::kStep * l;
-        p[i] = __ldg(reinterpret_cast<const uint4*>(at));
-        q[i] = __ldg(reinterpret_cast<const uint4*>(at + D / 2));
+        p[i] = *reinterpret_cast<const uint4*>(at);
+        q[i] = *reinterpret_cast<const uint4*>(at + D / 2);
     }
     r.a = Raw8<T>::get(p);
     r.b = Raw8<T>::get(q);

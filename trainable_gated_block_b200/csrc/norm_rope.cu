@@ -28,7 +28,7 @@ namespace {
 
 // Position of token row t; -1 (flagged) outside the table.
 __device__ __forceinline__ int token_pos(const NormRopeArgs& a, uint32_t t) {
-    const int pos = a.positions != nullptr ? __ldg(a.positions + t) : (int)(t % (uint32_t)a.S);
+    const int pos = a.positions != nullptr ? a.positions[t] : (int)(t % (uint32_t)a.S);
     if (pos < 0 || pos >= a.max_pos) {
         flag_status(a.status, kStatusBadData);
         return -1;
@@ -76,7 +76,7 @@ struct Bwd {
 // first, then the keys': 112.3 instead of 106.7 us for 32k tokens).
 template <typename T, int D>
 __global__ void __launch_bounds__(Fwd<T, D>::kThreads, Fwd<T, D>::kCtas)
-norm_rope_kernel(const NormRopeArgs a, uint32_t units, T* __restrict__ q_out, T* __restrict__ k_out) {
+norm_rope_kernel(const NormRopeArgs a, uint32_t units, T* q_out, T* k_out) {
     using S = Fwd<T, D>;
     constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16, kStage = S::kHeads * kRow;    // bytes from row to row, stage to stage
     extern __shared__ __align__(16) uint8_t smem[];
@@ -151,8 +151,8 @@ __device__ __forceinline__ void store_sums(float* p, int l, const Row& r) {
 // the result does not depend on timing.
 template <typename T, int D>
 __global__ void __launch_bounds__(Bwd<T, D>::kThreads, Bwd<T, D>::kCtas)
-norm_rope_bwd_kernel(const NormRopeArgs a, const T* __restrict__ dq_out, const T* __restrict__ dk_out,
-                     T* __restrict__ dq, T* __restrict__ dk, float* __restrict__ part, unsigned q_ctas) {
+norm_rope_bwd_kernel(const NormRopeArgs a, const T* dq_out, const T* dk_out, T* dq, T* dk, float* part,
+                     unsigned q_ctas) {
     using S = Bwd<T, D>;
     constexpr int kRow = 2 * Raw8<T>::kPieces * S::kThreads * 16;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -270,7 +270,7 @@ norm_rope_bwd_kernel(const NormRopeArgs a, const T* __restrict__ dq_out, const T
 // 32 rows of threads take every 32nd part. The first D / 32 CTAs add the query parts.
 template <int D>
 __global__ void __launch_bounds__(1024)
-norm_rope_dw_kernel(const float* __restrict__ part, int q_ctas, int ctas, float* __restrict__ dwq, float* __restrict__ dwk) {
+norm_rope_dw_kernel(const float* part, int q_ctas, int ctas, float* dwq, float* dwk) {
     __shared__ float acc[32][32];
     after_previous();
     const bool is_k = blockIdx.x >= D / 32;
