@@ -92,7 +92,7 @@ sas_status sas_get_error_flag(void *stream);
  *          blocks (requires ld_s >= n_rows).
  *          Else decode: device int32 [B]; every row of batch entry b has
  *          nh = (kv_len[b] - 1) / block_size history blocks (kv_len[b] >= 1;
- *          nh > ld_s is flagged and clamped to ld_s).
+ *          nh > ld_s is flagged and clamped to ld_s). 0 is a padding entry: nh = 0.
  *          Rows hold at most 16384 history blocks (1M tokens); longer rows
  *          return SAS_ERR_UNSUPPORTED.
  * K        budget in blocks, K >= 0. A row keeps min(K, nh) blocks.
@@ -270,7 +270,8 @@ sas_status sas_pool_pages(const void *k_cache, int num_pages, int Hkv, int D, in
  * kv_len[n]-1, history blocks j < (kv_len[n]-1)/64) and KV head h:
  *   s[n, h, j] = mean over the G query heads of h of q[n] . kpool[page_table[n, j], h]
  *                / sqrt(D) + noise[n, h, j]
- * then idx, cnt, log_gate, lse_s exactly as sas_select in decode mode.
+ * then idx, cnt, log_gate, lse_s exactly as sas_select in decode mode (kv_len[n] = 0:
+ * a padding entry without history).
  *
  * q          device bf16 [N, Hq, D]; kpool from sas_pool_pages.
  * page_table device int32 [N, max_pages]; a bad page id is flagged and the
@@ -306,7 +307,8 @@ size_t sas_decode_workspace_size(int N, int Hq, int Hkv, int D, int K);
  * page_table device int32 [N, max_pages]: logical block -> page id. Entries
  *            0..ceil(kv_len[n]/64)-1 must lie in [0, num_pages); a bad id is
  *            flagged and its block skipped.
- * kv_len     device int32 [N], 1 <= kv_len[n] <= 64*max_pages.
+ * kv_len     device int32 [N], 1 <= kv_len[n] <= 64*max_pages; 0 is a padding entry:
+ *            o 0, lse -inf, not flagged.
  * idx, cnt, log_gate   device [N, Hkv, K], [N, Hkv], [N, Hkv, K] from
  *            sas_select (decode mode).
  * o          device bf16 [N, Hq, D] (output). lse: device fp32 [N, Hq] or NULL.
@@ -367,7 +369,7 @@ size_t sas_decode_q8_workspace_size(int N, int Hq, int Hkv, int D, int K);
  *            v_scale * code, for the rows of that page and KV head. Between 2^-100
  *            and 2^120 for every page that is read; any other scale is flagged and
  *            its block skipped, like a bad page id.
- * kv_len     as in sas_decode_paged; 0 is a padding entry: o 0, lse -inf, not flagged.
+ * kv_len     as in sas_decode_paged.
  * log_gate   -inf (or the lowest fp32 value) leaves its block out: its page id, scales
  *            and page are not looked at. A block that idx names twice is attended twice.
  * Other arguments as in sas_decode_paged. Logits, softmax sums and accumulators are

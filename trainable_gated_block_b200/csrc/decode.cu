@@ -96,7 +96,7 @@ __device__ __forceinline__ ItemInfo item_info(const Params& p, int item, bool fl
         n_sel = max(0, min(n_sel, hi));
     }
     r.n_sel = n_sel;
-    if (!r.ok && flag) flag_status(p.status, kStatusBadData);
+    if (!r.ok && r.L != 0 && flag) flag_status(p.status, kStatusBadData);      // 0: a padding entry
     return r;
 }
 
@@ -415,8 +415,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 }
 
 __global__ void __launch_bounds__(kD)
-decode_combine_kernel(const float* part_o, const float* part_ml, int nslot, int Hq, int Hkv, int G, int K, long long V,
-                      int grid, __nv_bfloat16* o, float* lse) {
+decode_combine_kernel(const float* part_o, const float* part_ml, int nslot, const int32_t* kv_len, int Hq, int Hkv, int G,
+                      int K, long long V, int grid, __nv_bfloat16* o, float* lse) {
     // launched as a programmatic dependent of decode_kernel: its blocks may be
     // resident before the decode grid ends; wait for that grid's writes here (which
     // may not be read by the read-only path: dependent.cuh)
@@ -439,6 +439,7 @@ decode_combine_kernel(const float* part_o, const float* part_ml, int nslot, int 
             acc = fmaf(part_o[(row * nslot + s) * kD + d], w, acc);
         }
     }
+    if (kv_len[n] == 0) Lsum = 1.f, M = -INFINITY;      // a padding entry: o 0, lse -inf
     o[row * kD + d] = __float2bfloat16_rn(acc / Lsum);
     if (lse != nullptr && d == 0) lse[row] = (M + log2f(Lsum)) * kLn2;
 }
@@ -519,8 +520,8 @@ cudaError_t launch_decode(const DecodeArgs& a, void* workspace, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel, (const float*)part_o, (const float*)part_ml, lay.nslot, a.Hq,
-                           a.Hkv, G, a.K, lay.V, lay.grid, (__nv_bfloat16*)a.o, a.lse);
+    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel, (const float*)part_o, (const float*)part_ml, lay.nslot, a.kv_len,
+                           a.Hq, a.Hkv, G, a.K, lay.V, lay.grid, (__nv_bfloat16*)a.o, a.lse);
     if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();

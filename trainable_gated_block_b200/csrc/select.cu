@@ -32,7 +32,7 @@ struct RowCtx {
 };
 
 // History length of selection row `row` (= (b, h, r) flattened).
-//  decode (kv_len != null): nh = (kv_len[b] - 1) / 64
+//  decode (kv_len != null): nh = (kv_len[b] - 1) / 64, 0 for a padding entry (kv_len[b] = 0)
 //  prefill: nh = r; with per-sequence lengths (cu != null) rows r >= ceil(len_b / 64) are padding
 __device__ __forceinline__ RowCtx row_ctx(long long row, int Hkv, int n_rows, int ld_s, int cap,
                                           const int32_t* __restrict__ kv_len, const int32_t* __restrict__ cu,
@@ -45,7 +45,7 @@ __device__ __forceinline__ RowCtx row_ctx(long long row, int Hkv, int n_rows, in
     if (kv_len != nullptr) {
         const int L = kv_len[b];
         c.nh = (L >= 1) ? (L - 1) / kBlock : 0;
-        if (L < 1 && leader) flag_status(status, kStatusBadData);
+        if (L < 0 && leader) flag_status(status, kStatusBadData);      // 0: a padding entry
     } else if (cu != nullptr) {
         const int len = cu[b + 1] - cu[b];
         if (len < 0 && leader) flag_status(status, kStatusBadData);

@@ -322,7 +322,8 @@ def decode_workspace_bytes(N: int, Hq: int, Hkv: int, D: int, K: int) -> int:
 
 def decode_paged(q, k_cache, v_cache, page_table, kv_len, idx, cnt, log_gate, sm_scale=None,
                  page_size: int = 64, workspace=None, with_lse: bool = True):
-    """Paged decode. q [N,Hq,D]; caches [P,Hkv,64,D]. Returns o [N,Hq,D] and lse [N,Hq] (or None)."""
+    """Paged decode. q [N,Hq,D]; caches [P,Hkv,64,D]; kv_len 0 is a padding entry (o 0, lse -inf).
+    Returns o [N,Hq,D] and lse [N,Hq] (or None)."""
     _contig(q, k_cache, v_cache, page_table, kv_len, idx, cnt, log_gate)
     N, Hq, D = q.shape
     P, Hkv = k_cache.shape[0], k_cache.shape[1]
@@ -433,8 +434,7 @@ def _workspace(workspace, need: int, dev: int, like):
 def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, sm_scale=None,
                     page_size: int = 64, workspace=None, with_lse: bool = True):
     """Paged decode over 8-bit pages: caches [P,Hkv,64,D] float8_e4m3fn, scales [P,Hkv] fp32 (a key is
-    k_scale * code). Other arguments as in decode_paged; kv_len 0 is a padding entry (o 0, lse -inf).
-    Returns o [N,Hq,D] and lse [N,Hq] (or None)."""
+    k_scale * code). Other arguments as in decode_paged. Returns o [N,Hq,D] and lse [N,Hq] (or None)."""
     N, Hq, D = q.shape
     P, Hkv = k_cache.shape[:2]
     K = idx.shape[-1]
