@@ -240,7 +240,7 @@ __device__ __forceinline__ void page_rows(const AppendArgs& a, bool is_v, int pa
     const f2 u = f2_pack(unit, unit), n = f2_pack(1.f / kPageRows, 1.f / kPageRows);
     f2* out = reinterpret_cast<f2*>(a.kpool + head * D + sum_dim<D>(lane));
 #pragma unroll
-    for (int i = 0; i < SlotSum<D>::kKept; ++i) out[i] = f2_mul(f2_mul(mean.v[i], u), n);
+    for (int i = 0; i < SlotSum<D>::kKept; ++i) out[i] = f2_mul(f2_mul(mean.v[i], n), u);    // (64 keys times a scale of 2^120 have no fp32 sum)
 }
 
 // ------------------------------------------------------------------ single tokens
@@ -755,7 +755,7 @@ append_blocks_kernel(const AppendArgs a, uint32_t kv_works, uint32_t q_units, ui
 #pragma unroll
                     for (int n = 1; n < kPerWarp; n *= 2) total += __shfl_xor_sync(0xffffffffu, total, n);
                     const float s = unit[i];
-                    if (r == 0 && s > 0.f) a.kpool[(head0 + u.part + i * parts) * D + d] = total * s * (1.f / kPageRows);
+                    if (r == 0 && s > 0.f) a.kpool[(head0 + u.part + i * parts) * D + d] = total * (1.f / kPageRows) * s;
                 }
             }
         };
