@@ -138,3 +138,14 @@ def test_a_closed_block_is_left_out_whatever_its_page_and_scales():
             x["k_scale"][page], x["v_scale"][page] = b, b
     got = _run(x)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("size", [-133, -127, -120, -60, 0, 60, 100])
+def test_queries_of_any_size(size):
+    """Query rows down to bf16's subnormals beside key scales that make their logits count, and large ones."""
+    x = _make([64 * 5 + 3, 200, 64 * 4], 8, 2, 3, seed=97)
+    q = torch.randint(-7, 8, x["q"].shape, generator=torch.Generator().manual_seed(98)).double() * 2.0 ** size
+    x["q"] = q.to(torch.bfloat16)
+    assert torch.equal(x["q"].double(), q)
+    x["k_scale"] = x["k_scale"] * 2.0 ** min(max(-size - 2, -90), 125)
+    _check(_run(x, sm_scale=0.5), _ref(x, 0.5))

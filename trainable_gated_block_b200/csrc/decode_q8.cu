@@ -321,9 +321,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e with top 2^e in [2^13, 2^14); 1 for a zero or infinite row
+        // 2^e with top 2^e in [2^13, 2^14), or at most 2^126 (rows below 2^-112, down to subnormals); 1 for an infinite row
         const int te = (int)(__float_as_uint(top) >> 23);           // biased exponent of top
-        const int e = te == 0 || te == 255 ? 0 : min(13 + 127 - te, 126);
+        const int e = te == 255 ? 0 : min(13 + 127 - te, 126);
         const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
