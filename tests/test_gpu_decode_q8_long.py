@@ -10,7 +10,6 @@ from tests.test_gpu_decode_q8_range import shared
 from trainable_gated_block_b200 import build, sas
 
 pytestmark = pytest.mark.gpu
-RANGE_WARPS = 4             # an SM, of the device's ranges
 CLUSTER_WARPS = (32, 24, 16, 12, 8, 6, 4, 3)     # of an item
 
 
@@ -29,12 +28,14 @@ def _slots_of_a_warp(N, Hq, Hkv, K):
         # clusters: resident together as far as that goes, twelve warps an SM
         warps = next((w for w in CLUSTER_WARPS if N * Hkv * w <= 12 * sms), CLUSTER_WARPS[-1])
         return -(-(K + 1) // warps)
-    return -(-N * Hkv * (K + 1) // (RANGE_WARPS * sms))
+    slots = N * Hkv * (K + 1)
+    return -(-slots // ((4 if slots <= 32 * 4 * sms else 10) * sms))        # ranges of four or of ten warps an SM
 
 
 @pytest.mark.parametrize("N,Hq,Hkv,K,ranges,fewest", [
-    (75, 8, 8, 66, True, 65), (75, 32, 8, 70, True, 65),        # ranges over the ends of items
-    (2, 16, 8, 2500, True, 65),                                 # ranges within an item
+    (75, 8, 8, 30, True, 32), (2, 16, 8, 1180, True, 32),       # ranges of four warps: one full batch
+    (75, 8, 8, 66, True, 27), (75, 32, 8, 70, True, 27),        # of ten warps, over the ends of items
+    (75, 40, 8, 170, True, 65), (3, 8, 8, 4100, True, 65),      # the same, within an item
     (64, 8, 8, 330, False, 65), (64, 40, 8, 290, False, 65),    # three warps an item
     (8, 32, 8, 2100, False, 65),                                # 24 warps an item
     (24, 16, 8, 530, False, 65)])                               # eight

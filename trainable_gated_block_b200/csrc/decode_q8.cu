@@ -13,10 +13,11 @@
 // range for 2^20 tokens: they are kept times 2^-36.)
 // Codes are exact in fp16, the queries are scaled by a power of two (their
 // largest element to 2^13 .. 2^14, what falls out of fp16 below is under 2^-30 of
-// it), a weight is the sum of two fp16 numbers (2^-21 relative: one alone, 2^-11 off,
-// let one output in 50 round to another bf16 number); logits, sums and accumulators
-// are fp32. The second numbers' product costs nothing where up to four heads share a
-// KV head, since they take the columns that these leave empty.
+// it), a weight is the sum of two fp16 numbers (2^-21 relative; one alone, 2^-11 off,
+// made outputs differ by 4 to 6 parts in 10^4 of their norm); logits, sums and
+// accumulators are fp32. Where up to four heads share a KV head the second numbers take
+// the columns that these leave empty, which costs 64 x 33 slots of 8 KV heads 48.9 ->
+// 49.3 us and 8 x 1025 165.7 -> 167.3; a product of their own, as beyond four, 49.3 and 171.9.
 //
 // HBM-bound design. Each (sequence, KV head) item has K + 1 slots: its kept blocks and
 // the current one. The warps of a cluster of one to eight CTAs cut an item's slots
@@ -41,8 +42,8 @@
 // joins them.
 //
 // Measured on one B200 (32/8 heads): eight 64k sequences with all history 164 us, 6.57
-// TB/s of codes (by ranges 171); 64 sequences at 8k-64k, K = 32: 51.2 us, 5.3 TB/s (by
-// ranges 55.6); one sequence at 8k, K = 16: 6.8 us (8.6), the latency of a launch, the
+// TB/s of codes (by ranges 186); 64 sequences at 8k-64k, K = 32: 50.8 us, 5.4 TB/s (by
+// ranges 55.0); one sequence at 8k, K = 16: 7.0 us (9.6), the latency of a launch, the
 // chain selection entry -> page -> tile, one block's math and the join. A
 // variant with a producer warp, consumers that meet at each item's end and
 // one exp2f for each logit took 237 and 81.6 us: its math did not keep up.
@@ -88,10 +89,13 @@ constexpr int kList = 64;                           // two batches of a warp
 // warps an SM (their rings are its shared memory).
 constexpr int kSmWarps = 12;
 // Without clusters the slots of all items are one line, cut into a range for each
-// warp of the device: a CTA of four warps with three stages each an SM. (Measured
-// against ten warps of one stage: 16,400 slots 51.9 / 55.1 us, 24,024 slots 71.3 / 71.5,
-// 77,400 slots 205 / 200.)
-constexpr int kRangeWarps = 4, kRangeStages = 3;
+// warp of the device: a CTA of four warps with three stages each an SM, or, where their
+// ranges would be longer than the 32 slots that a warp resolves at a time, of ten warps
+// of one stage, which have more math under way. (Measured, four / ten: 1,032 slots
+// 12.8 / 12.6 us, 8,200 slots 31.6 / 33.5, 16,400 slots 51.9 / 55.3, 19,800 slots
+// 62.9 / 62.7, 24,024 slots 72.2 / 71.3, 39,000 slots 111.9 / 109.2, 77,400 slots 217 / 202;
+// of five heads a KV head 16,400 slots 51.4 / 56.7, 77,400 slots 230 / 209.)
+constexpr int kRangeWarps = 4, kRangeStages = 3, kLongRangeWarps = 10, kLongRangeStages = 1;
 
 // kWarps warps of a CTA, kDepth ring stages each, and their shared memory.
 template <int kWarps, int kDepth>
@@ -691,7 +695,7 @@ decode_q8_combine_kernel(const float* part_o, const float* part_ml, int nslot, i
 
 struct Layout {
     long long V;
-    int warps, ctas;            // of a cluster's CTA, of a cluster; ctas 0: ranges
+    int warps, ctas;            // of a CTA, of a cluster; ctas 0: ranges
     int grid, ranges, nslot;
 };
 constexpr struct {
@@ -704,11 +708,18 @@ constexpr struct {
 // that not all places can be had: an eighth is left out.) Where one round does, the
 // fewest warps; else the most. Left to the ranges: few items with many slots (the
 // clusters' warps would be under half of what the device holds), and odd waves.
-// Measured (us, 8 KV heads, sequences x (K + 1): this choice / ranges and combine):
-// 1 x 17 6.9 / 8.6, 1 x 33 8.5 / 8.9 but 2 x 33 9.5 / 9.0 and 1 x 129 13.1 / 11.1,
-// 8 x 17 9.0 / 11.6, 4 x 33 10.7 / 9.8, 4 x 65 14.2 / 15.0, 8 x 33 13.3 / 15.9, 24 x 33
-// 25.0 / 27.9, 48 x 33 40.1 / 45.4, 64 x 33 50.7 / 55.6, 128 x 33 91.8 / 99.4, 8 x 1025
-// 164.8 / 171.2; with a last wave of a third: 72 x 33 66.1 / 60.0.
+// Measured (us, clusters / ranges and combine; items x slots, an item being a sequence
+// and KV head; eight items are one sequence of 8 KV heads, or eight of one):
+//   8 x 17 7.0 / 9.6, 32 x 17 8.8 / 8.8, 64 x 17 10.3 / 14.2, 128 x 17 13.3 / 16.3,
+//   64 x 33 14.2 / 17.1, 128 x 33 18.2 / 21.0, 192 x 33 24.4 / 27.8, 384 x 33 39.3 / 44.4,
+//   512 x 33 49.7 / 55.0, 576 x 33 54.6 / 61.5, 1024 x 33 91.9 / 100.1, 32 x 65 15.3 / 15.6,
+//   64 x 65 18.1 / 22.6, 192 x 65 39.5 / 43.4, 512 x 65 89.3 / 96.7, 64 x 1025 169 / 186;
+// left to the ranges:
+//   8 x 33 9.1 / 8.9, 16 x 33 10.2 / 9.1, 24 x 33 11.4 / 10.8, 8 x 65 11.4 / 9.7,
+//   16 x 65 13.0 / 11.8, 24 x 65 14.2 / 13.7, 8 x 129 15.9 / 13.1, 16 x 129 17.3 / 16.3, and
+//   with a last wave of a third 600 x 33 66.0 / 62.9, 640 x 33 66.9 / 66.2, 600 x 65 120 / 112.
+// At 32 x 33 (two rounds of 32 warps for one slot more than they have) the rule takes the
+// slower: 12.2 / 11.3.
 bool choose_clusters(long long items, int slots, int sms, int& cta_warps, int& ctas) {
     long long best = 0;
     for (const auto& c : kClusters) {
@@ -731,16 +742,19 @@ Layout layout(int N, int Hkv, int K) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
     r.V = (long long)N * Hkv * (K + 1);
+    if (choose_clusters((long long)N * Hkv, K + 1, sms, r.warps, r.ctas)) {
+        r.grid = N * Hkv * r.ctas;
+        r.ranges = r.nslot = 0;
+        return r;
+    }
+    r.ctas = 0;
+    r.warps = r.V > 32LL * kRangeWarps * sms ? kLongRangeWarps : kRangeWarps;
     r.grid = (int)(r.V < sms ? r.V : sms);
-    const long long most = (long long)sms * kRangeWarps;
+    const long long most = (long long)sms * r.warps;
     r.ranges = (int)(r.V < most ? r.V : most);
     const long long mn = r.V / r.ranges;                     // shortest range
     const long long span = (K + 1 + mn - 1) / mn + 1;        // ranges one item's slots can touch
     r.nslot = (int)(span < r.ranges ? span : r.ranges);
-    if (choose_clusters((long long)N * Hkv, K + 1, sms, r.warps, r.ctas))
-        r.grid = N * Hkv * r.ctas;
-    else
-        r.ctas = 0;
     return r;
 }
 
@@ -812,7 +826,8 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, const float* k_scale, const fl
         if (e == cudaSuccess) count_launches(1);
         return e;
     }
-    e = launch<kRangeWarps, kRangeStages>(lay, map, p, st);
+    e = lay.warps == kRangeWarps ? launch<kRangeWarps, kRangeStages>(lay, map, p, st)
+                                 : launch<kLongRangeWarps, kLongRangeStages>(lay, map, p, st);
     if (e != cudaSuccess) return e;
     count_launches(1);
     // (501 partials of a row: 13.5 us with eight groups, 14.8 with four; 34 partials: 12.0, 11.5)
