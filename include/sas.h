@@ -469,6 +469,9 @@ sas_status sas_qk_norm_rope_bwd(sas_dtype dtype, const void *dq_out, const void 
  * q_out and k_out that belong to no sequence, or to a skipped one, are left as they are.
  * Outputs must not overlap the inputs. D in {64, 128}, page_size 64; T * Hq, T * Hkv
  * and (T / 64 + 2 N) * Hkv below 2^29.
+ * The decode calls read pages of D = 128 only: pages of D = 64 are for a caller's own
+ * attention. No call attends from several new tokens to a cached history: after a
+ * piece of a prompt behind cached tokens, q_out too is for a caller's own attention.
  */
 sas_status sas_append_paged(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
                             int64_t ld_v, const void *q_weight, const void *k_weight,
@@ -487,7 +490,8 @@ sas_status sas_append_paged(const void *q, int64_t ld_q, const void *k, int64_t 
  *            whatever they held before: the least power of two s (not under 2^-64) with
  *            |x| <= 448 s for all new values of that page and head. Later rows keep the
  *            scale if they fit it; else it grows by the same rule and the older rows' codes
- *            are expressed in it (exactly, but for codes that fall below the normal range).
+ *            are expressed in it (exactly, but for codes that fall below the normal range;
+ *            where an old scale of another origin is no power of two they are rounded anew).
  *            Codes are rounded to nearest even. A NaN or an infinity is stored as NaN and
  *            has no part in the scale. An older scale outside 2^-100 .. 2^120 is flagged
  *            and the page skipped.

@@ -98,7 +98,7 @@ def page_items(kv_len, cu_new, T, page_table):
 
 
 def decode_q8(q, k_codes, v_codes, k_scale, v_scale, page_table, kv_len, idx, cnt, log_gate, sm_scale):
-    """o, lse and their error bounds for fp32 logits and fp16 probabilities (see the body)."""
+    """o, lse and their error bounds for fp32 logits and probabilities of two fp16 numbers (see the body)."""
     q, kc, vc = f64(q), f64(k_codes), f64(v_codes)
     ks, vs = f64(k_scale), f64(v_scale)
     pt, kv_len = page_table.cpu().numpy(), kv_len.cpu().numpy()

@@ -589,7 +589,8 @@ def append_paged(q, k, v, table, k_cache, v_cache, page_table, kv_len, q_weight=
     q [T,Hq,D], k, v [T,Hkv,D] bf16 (token rows may be strided). kv_len [N] counts the new tokens. One token
     for each sequence (T = N; kv_len 0: a padding entry), or with cu_new int32 [N+1] the rows
     cu_new[n]..cu_new[n+1]-1 of each, at most max_new. kpool [P,Hkv,D]: filled pages get their mean key.
-    Returns the rotated q [T,Hq,D]; with_k: q and the rotated k [T,Hkv,D]."""
+    Returns the rotated q [T,Hq,D]; with_k: q and the rotated k [T,Hkv,D], as attn_fwd_varlen takes them for
+    whole prompts. (Pieces behind cached tokens are stored, but no call attends from them to the cache.)"""
     return _append(False, q, k, v, table, k_cache, v_cache, (), page_table, kv_len, q_weight, k_weight, cu_new,
                    max_new, eps, kpool, with_k, page_size)
 
