@@ -37,10 +37,11 @@ def test_no_read_only_loads_where_kernels_start_early():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("K", [3, 120])
-def test_calls_back_to_back_have_the_bits_of_calls_one_by_one(K):
-    """Steps of norm + rotation, append into 8-bit pages and decode, each reading what the call in front has
-    written (queries, keys, pages, scales that grow), with every step's result kept."""
+@pytest.mark.parametrize("K,scored", [(3, False), (120, False), (3, True), (100, True)])
+def test_calls_back_to_back_have_the_bits_of_calls_one_by_one(K, scored):
+    """Steps of norm + rotation, append into 8-bit pages, scores and selection (or a fixed one) and decode, each
+    reading what the call in front has written (queries, keys, pages, scales that grow, mean keys, selections),
+    with every step's result kept."""
     if not torch.cuda.is_available():
         pytest.skip("needs a CUDA GPU")
     build.build()
@@ -64,16 +65,20 @@ def test_calls_back_to_back_have_the_bits_of_calls_one_by_one(K):
 
     def run(wait):
         pages = [t.cuda() for t in codes] + [t.cuda() for t in scales]
+        kpool = pages[0].float().mean(2) * pages[2][:, :, None]
         out = []
         torch.cuda.synchronize()
         for i in range(steps):
             q, k = sas.qk_norm_rope(qkv[0][i], qkv[1][i], table, *w, positions=lens[i])
             if wait:
                 torch.cuda.synchronize()
-            q = sas.append_paged_q8(q, k, qkv[2][i], table, *pages, pt, lens[i], *w)
+            q = sas.append_paged_q8(q, k, qkv[2][i], table, *pages, pt, lens[i], *w, kpool=kpool)
             if wait:
                 torch.cuda.synchronize()
-            out.append((q, *sas.decode_paged_q8(q, *pages, pt, lens[i], *sel)))
+            kept = sas.score_select_decode(q, kpool, pt, lens[i], K, blocks)[1:4] if scored else sel
+            if wait:
+                torch.cuda.synchronize()
+            out.append((q, kpool.clone(), *sas.decode_paged_q8(q, *pages, pt, lens[i], *kept)))
             if wait:
                 torch.cuda.synchronize()
         torch.cuda.synchronize()
